@@ -19,6 +19,12 @@ DSA_BF16 = 0
 DSA_E4M3 = 1
 DSA_E4M3_UE8M0 = 2
 
+DSA_ROPE_HALF = 0
+DSA_ROPE_INTERLEAVED = 1
+DSA_ROPE_BF16 = 0
+DSA_ROPE_FP16 = 1
+DSA_ROPE_FP32 = 2
+
 _STATUS = {
     0: "DSA_OK",
     1: "DSA_ERR_INVALID_ARG",
@@ -42,6 +48,12 @@ EXPORTED = (
     "dsa_forward_noalloc_scratch_bytes",
     "dsa_check_device_errors",
     "dsa_cache_write",
+    "dsa_cache_write_fp8",
+    "dsa_paged_plan",
+    "dsa_rope",
+    "dsa_rope_frequencies",
+    "dsa_sparse_mla_fp8_workspace_size",
+    "dsa_sparse_mla_fp8_fwd",
     "dsa_set_debug_checks",
     "dsa_selftest_bounded_wait",
     "dsa_status_string",
@@ -80,6 +92,26 @@ class DsaProblem(ctypes.Structure):
     ]
 
 
+class DsaRope(ctypes.Structure):
+    """Mirror of ``dsa_rope_desc_t``."""
+
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rope_begin", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("x_token_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("transposed", ctypes.c_int32),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -115,6 +147,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.dsa_check_device_errors.argtypes = [P]
     lib.dsa_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
     lib.dsa_cache_write.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P]
+    lib.dsa_cache_write_fp8.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, ctypes.c_int, P, P, P, P, P]
+    lib.dsa_paged_plan.argtypes = [i32, P, P, P, i32, P, i32, P, i32, P, P, P, P, i32, P, P]
+    lib.dsa_rope.argtypes = [ctypes.POINTER(DsaRope), P, P, P, P, P]
+    dbl = ctypes.c_double
+    lib.dsa_rope_frequencies.argtypes = [i32, dbl, dbl, dbl, dbl, dbl, P, ctypes.POINTER(dbl)]
+    lib.dsa_sparse_mla_fp8_workspace_size.argtypes = [pp]
+    lib.dsa_sparse_mla_fp8_workspace_size.restype = sz
+    lib.dsa_sparse_mla_fp8_fwd.argtypes = [pp, P, P, P, P, P, P, P, sz, P]
     lib.dsa_set_debug_checks.argtypes = [i32]
     lib.dsa_set_debug_checks.restype = None
     lib.dsa_status_string.argtypes = [ctypes.c_int]
@@ -122,7 +162,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.dsa_abi_version.restype = i32
     for name in ("dsa_indexer_scores", "dsa_topk", "dsa_indexer_topk_streaming", "dsa_sparse_mla_fwd", "dsa_dense_mla_fwd", "dsa_forward",
                  "dsa_forward_noalloc",
-                 "dsa_check_device_errors", "dsa_selftest_bounded_wait", "dsa_cache_write"):
+                 "dsa_check_device_errors", "dsa_selftest_bounded_wait", "dsa_cache_write", "dsa_cache_write_fp8",
+                 "dsa_paged_plan", "dsa_rope", "dsa_rope_frequencies", "dsa_sparse_mla_fp8_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -270,6 +311,123 @@ def dsa_cache_write(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_n
     _check(lib.dsa_cache_write(int(positions.numel()), _ptr(k_idx_raw), _ptr(kv_raw), _ptr(positions), _ptr(rows),
                                _ptr(k_norm_w), _ptr(k_norm_b), _ptr(kv_norm_w), _ptr(inv_freq), eps,
                                _ptr(k_idx_cache), _ptr(kv_cache), _stream(stream)), "dsa_cache_write")
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(first: torch.Tensor, *rest) -> None:
+    """Every tensor on the first one's device, and that device current: the launch goes to the
+    current device, and a stream of another one would not order it."""
+    _need(first.is_cuda, "libdsa takes device tensors only")
+    dev = first.device
+    for t in rest:
+        _need(t is None or t.device == dev, "libdsa takes tensors of one device")
+    _need(dev.index == torch.cuda.current_device(), "the tensors' device must be the current device")
+
+
+def dsa_paged_plan(len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts, n_pages: int,
+                   free_head=None, stream=None) -> None:
+    """Sequence offsets, slot map and block-table entries of one step, from the requests'
+    lengths (see include/dsa.h).  ``positions`` and ``rows`` may be longer than the step's
+    tokens (padding gets position 0 and row -1); ``counts`` [4] receives the new tokens, the
+    pages taken, the longest sequence and the error bits."""
+    _same_device(len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts, free_head)
+    tensors = (len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts)
+    _need(all(t.dtype == torch.int32 for t in tensors) and (free_head is None or free_head.dtype == torch.int32),
+          "dsa_paged_plan takes int32 tensors")
+    B, T = len_cached.numel(), positions.numel()
+    _need(len_new.numel() == B and cu_q.numel() == B + 1 and cu_k.numel() == B + 1 and counts.numel() == 4
+          and rows.numel() == T and block_table.dim() == 2 and block_table.shape[0] == B
+          and (free_head is None or free_head.numel() == 1), "dsa_paged_plan: shapes do not agree")
+    lib = load()
+    _check(lib.dsa_paged_plan(B, _ptr(len_cached), _ptr(len_new), _ptr(block_table), block_table.shape[1],
+                              _ptr(free_pages), free_pages.numel(), _ptr(free_head), n_pages, _ptr(cu_q), _ptr(cu_k),
+                              _ptr(positions), _ptr(rows), T, _ptr(counts), _stream(stream)), "dsa_paged_plan")
+
+
+_ROPE_TYPES = {torch.bfloat16: DSA_ROPE_BF16, torch.float16: DSA_ROPE_FP16, torch.float32: DSA_ROPE_FP32}
+
+
+def dsa_rope(x, positions, inv_freq, out, layout: int = DSA_ROPE_INTERLEAVED, rope_begin: int = 0,
+             rope_dim: Optional[int] = None, scale: float = 1.0, transposed: bool = False, stream=None) -> None:
+    """Rotary positions on dims ``rope_begin .. + rope_dim`` of ``x`` [tokens, heads, head_dim]
+    into ``out`` (same shape and type; ``out`` may be ``x``).  Both may be slices of wider
+    tensors: only the last dimension has to be dense."""
+    _same_device(x, positions, inv_freq, out)
+    _need(x.dim() == 3 and x.shape == out.shape, "dsa_rope takes x and out [tokens, heads, head_dim]")
+    _need(x.dtype in _ROPE_TYPES and out.dtype == x.dtype, "dsa_rope takes bf16, fp16 or fp32, the same for x and out")
+    T, H, D = x.shape
+    if rope_dim is None:
+        rope_dim = D - rope_begin
+    _need((x.stride(2) == 1 and out.stride(2) == 1) or D == 1, "dsa_rope: the last dimension must be dense")
+    _need(positions.dtype == torch.int32 and positions.numel() == T, "dsa_rope: positions must be int32 [tokens]")
+    _need(inv_freq.dtype == torch.float32 and 2 * inv_freq.numel() == rope_dim, "dsa_rope: inv_freq must be fp32 [rope_dim / 2]")
+    r = DsaRope(T, H, D, rope_begin, rope_dim, layout, _ROPE_TYPES[x.dtype], x.stride(0), x.stride(1), out.stride(0),
+                out.stride(1), scale, 1 if transposed else 0)
+    _check(load().dsa_rope(ctypes.byref(r), ctypes.c_void_p(x.data_ptr()), _ptr(positions), _ptr(inv_freq),
+                           ctypes.c_void_p(out.data_ptr()), _stream(stream)), "dsa_rope")
+
+
+def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: float = 4096.0,
+                         beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """RoPE frequencies (a host fp32 tensor [rope_dim / 2]) and the attention factor; ``factor``
+    > 1 stretches them for long contexts (see include/dsa.h)."""
+    freq = torch.empty(max(rope_dim, 0) // 2, dtype=torch.float32)
+    att = ctypes.c_double()
+    _check(load().dsa_rope_frequencies(rope_dim, base, factor, original_len, beta_fast, beta_slow,
+                                       ctypes.c_void_p(freq.data_ptr()), ctypes.byref(att)), "dsa_rope_frequencies")
+    return freq, att.value
+
+
+def dsa_cache_write_fp8(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache,
+                        k_scale_cache, kv_cache, kv_scale_cache, idx_dtype: int = DSA_E4M3_UE8M0, eps: float = 1e-6,
+                        stream=None) -> None:
+    """dsa_cache_write into an 8-bit cache: the indexer key as ``idx_dtype`` says, the latent as
+    640 e4m3 codes and one ue8m0 scale per row (see include/dsa.h)."""
+    n = positions.numel()
+    _same_device(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache, k_scale_cache,
+                 kv_cache, kv_scale_cache)
+    key, scale = {DSA_BF16: (torch.bfloat16, None), DSA_E4M3: (torch.uint8, torch.float32),
+                  DSA_E4M3_UE8M0: (torch.uint8, torch.uint8)}.get(idx_dtype, (None, None))
+    _need(key is not None, "dsa_cache_write_fp8: idx_dtype must be DSA_BF16, DSA_E4M3 or DSA_E4M3_UE8M0")
+    _need(k_idx_raw.dtype == torch.bfloat16 and kv_raw.dtype == torch.bfloat16 and k_idx_raw.numel() == 128 * n
+          and kv_raw.numel() == 576 * n, "dsa_cache_write_fp8: k_idx_raw must be bf16 [n, 128], kv_raw bf16 [n, 576]")
+    _need(positions.dtype == torch.int32 and rows.dtype == torch.int32 and rows.numel() == n,
+          "dsa_cache_write_fp8: positions and rows must be int32 [n]")
+    _need(all(w.dtype == torch.float32 and w.numel() == m for w, m in
+              ((k_norm_w, 128), (k_norm_b, 128), (kv_norm_w, 512), (inv_freq, 32))),
+          "dsa_cache_write_fp8: k_norm_w, k_norm_b fp32 [128], kv_norm_w fp32 [512], inv_freq fp32 [32]")
+    _need(k_idx_cache.dtype == key and k_idx_cache.shape[-1] == 128 and kv_cache.dtype == torch.uint8
+          and kv_cache.shape[-1] == 640 and kv_scale_cache.dtype == torch.uint8
+          and kv_scale_cache.numel() * 640 == kv_cache.numel(), "dsa_cache_write_fp8: cache types or shapes")
+    _need(k_scale_cache is None if scale is None else k_scale_cache is not None and k_scale_cache.dtype == scale
+          and k_scale_cache.numel() * 128 == k_idx_cache.numel(), "dsa_cache_write_fp8: k_scale_cache does not fit idx_dtype")
+    _check(load().dsa_cache_write_fp8(n, _ptr(k_idx_raw), _ptr(kv_raw), _ptr(positions), _ptr(rows), _ptr(k_norm_w),
+                                      _ptr(k_norm_b), _ptr(kv_norm_w), _ptr(inv_freq), eps, idx_dtype, _ptr(k_idx_cache),
+                                      _ptr(k_scale_cache), _ptr(kv_cache), _ptr(kv_scale_cache), _stream(stream)),
+           "dsa_cache_write_fp8")
+
+
+def dsa_sparse_mla_fp8_workspace_size(p: DsaProblem) -> int:
+    return int(load().dsa_sparse_mla_fp8_workspace_size(ctypes.byref(p)))
+
+
+def dsa_sparse_mla_fp8_fwd(p: DsaProblem, q, kv, kv_scale, idx, out, lse, workspace=None, stream=None) -> None:
+    """dsa_sparse_mla_fwd over the 8-bit latent cache (kv uint8 [S, 640], kv_scale uint8 [S])."""
+    _same_device(q, kv, kv_scale, idx, out, lse, workspace)
+    T = p.total_q
+    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16 and lse.dtype == torch.float32
+          and idx.dtype == torch.int32 and kv.dtype == torch.uint8 and kv_scale.dtype == torch.uint8,
+          "dsa_sparse_mla_fp8_fwd: q, out bf16, lse fp32, idx int32, kv and kv_scale uint8")
+    _need(q.numel() == T * 128 * 576 and out.numel() == T * 128 * 512 and lse.numel() == T * 128
+          and idx.numel() == T * p.topk and kv.numel() >= p.total_k * 640 and kv_scale.numel() >= p.total_k,
+          "dsa_sparse_mla_fp8_fwd: shapes do not fit the problem")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().dsa_sparse_mla_fp8_fwd(ctypes.byref(p), _ptr(q), _ptr(kv), _ptr(kv_scale), _ptr(idx), _ptr(out),
+                                         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), "dsa_sparse_mla_fp8_fwd")
 
 
 def dsa_set_debug_checks(enable: bool) -> None:

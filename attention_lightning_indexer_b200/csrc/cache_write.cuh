@@ -44,6 +44,7 @@ cache_write_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __nv_bf
     if (t >= n) return;                                       // whole warp
     const int p = __ldg(pos + t);
     const int64_t row = __ldg(rows + t);
+    if (row < 0) return;                                      // a token without a row (padding)
     // the 32 rotation angles of this position, pair i by lane i (both RoPEs use the same
     // frequencies); lanes read the ones they need by shuffles
     float c_lane, s_lane;

@@ -4,14 +4,19 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
 #include "../../include/dsa.h"
 #include "cache_write.cuh"
+#include "cache_write_fp8.cuh"
 #include "dsa_common.cuh"
 #include "indexer_tc.cuh"
+#include "paged_plan.cuh"
+#include "rope.cuh"
 #include "select_stream.cuh"
+#include "sparse_mla_fp8.cuh"
 #include "sparse_mla_pair.cuh"
 #include "topk.cuh"
 
@@ -141,6 +146,12 @@ dsa_status_t set_smem_attrs() {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(dsa::mla::sparse_mla_pair_kernel<false, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, dsa::mla::PairCfg::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dsa::mla8::sparse_mla_fp8_plain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dsa::mla8::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dsa::plan::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)dsa::plan::smem_bytes(dsa::plan::MAX_BATCH));
     if (e == cudaSuccess) e = indexer_attr<8, false, dsa::indexer::SCORES>();
     if (e == cudaSuccess) e = indexer_attr<8, true, dsa::indexer::SCORES>();
     if (e == cudaSuccess) e = indexer_attr<8, false, dsa::indexer::SAMPLE>();
@@ -656,6 +667,170 @@ dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void
         n_tokens, reinterpret_cast<const __nv_bfloat16 *>(k_idx_raw), reinterpret_cast<const __nv_bfloat16 *>(kv_raw),
         positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, eps, reinterpret_cast<__nv_bfloat16 *>(k_idx_cache),
         reinterpret_cast<__nv_bfloat16 *>(kv_cache));
+    return launch_status();
+}
+
+dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw, const int32_t *positions,
+                                 const int32_t *rows, const float *k_norm_w, const float *k_norm_b,
+                                 const float *kv_norm_w, const float *inv_freq, float eps, dsa_dtype_t idx_dtype,
+                                 void *k_idx_cache, void *k_scale_cache, void *kv_cache, void *kv_scale_cache,
+                                 dsa_stream_t stream) {
+    if (n_tokens < 0 || !(eps >= 0.0f) || isinf(eps)) return DSA_ERR_INVALID_ARG;
+    if (idx_dtype != DSA_BF16 && idx_dtype != DSA_E4M3 && idx_dtype != DSA_E4M3_UE8M0) return DSA_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return DSA_OK;
+    const void *ptrs[] = {k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache, kv_cache};
+    for (const void *q : ptrs)
+        if (q == nullptr || !aligned16(q)) return DSA_ERR_INVALID_ARG;
+    if (kv_scale_cache == nullptr || (idx_dtype == DSA_BF16) != (k_scale_cache == nullptr)) return DSA_ERR_INVALID_ARG;
+    if (idx_dtype == DSA_E4M3 && (reinterpret_cast<uintptr_t>(k_scale_cache) & 3u) != 0) return DSA_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)(((int64_t)n_tokens + dsa::cache::WARPS - 1) / dsa::cache::WARPS);
+    auto launch = [&](auto kernel) {
+        kernel<<<grid, 32 * dsa::cache::WARPS, 0, (cudaStream_t)stream>>>(
+            n_tokens, reinterpret_cast<const __nv_bfloat16 *>(k_idx_raw), reinterpret_cast<const __nv_bfloat16 *>(kv_raw),
+            positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, eps, static_cast<unsigned char *>(k_idx_cache),
+            k_scale_cache, static_cast<unsigned char *>(kv_cache), static_cast<unsigned char *>(kv_scale_cache));
+    };
+    if (idx_dtype == DSA_BF16) launch(dsa::cache::cache_write_fp8_kernel<dsa::cache::KEY_BF16>);
+    else if (idx_dtype == DSA_E4M3) launch(dsa::cache::cache_write_fp8_kernel<dsa::cache::KEY_E4M3>);
+    else launch(dsa::cache::cache_write_fp8_kernel<dsa::cache::KEY_UE8M0>);
+    return launch_status();
+}
+
+dsa_status_t dsa_paged_plan(int32_t batch, const int32_t *len_cached, const int32_t *len_new, int32_t *block_table,
+                            int32_t max_pages, const int32_t *free_pages, int32_t n_free, const int32_t *free_head,
+                            int32_t n_pages, int32_t *cu_q, int32_t *cu_k, int32_t *positions, int32_t *rows,
+                            int32_t n_tokens, int32_t *counts, dsa_stream_t stream) {
+    if (batch < 1 || n_tokens < 0 || max_pages < 1 || n_free < 0 || n_pages < 1 || n_pages >= (1 << 25))
+        return DSA_ERR_INVALID_ARG;
+    if (batch > dsa::plan::MAX_BATCH) return DSA_ERR_UNSUPPORTED;
+    const void *ptrs[] = {len_cached, len_new, block_table, cu_q, cu_k, counts};
+    for (const void *q : ptrs)
+        if (q == nullptr || (reinterpret_cast<uintptr_t>(q) & 3u) != 0) return DSA_ERR_INVALID_ARG;
+    if ((n_free > 0 && free_pages == nullptr) || (n_tokens > 0 && (positions == nullptr || rows == nullptr)))
+        return DSA_ERR_INVALID_ARG;
+    const void *more[] = {free_pages, free_head, positions, rows};
+    for (const void *q : more)
+        if ((reinterpret_cast<uintptr_t>(q) & 3u) != 0) return DSA_ERR_INVALID_ARG;
+    if (free_head != nullptr && free_head == counts + 1) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st;
+    if ((st = set_smem_attrs()) != DSA_OK) return st;
+    dsa::plan::Args a{batch, n_tokens, max_pages, n_free, n_pages, len_cached, len_new, block_table,
+                      free_pages, free_head, cu_q, cu_k, positions, rows, counts};
+    const unsigned grid = (unsigned)(((int64_t)n_tokens + dsa::plan::TOKENS - 1) / dsa::plan::TOKENS);
+    dsa::plan::paged_plan_kernel<<<grid > 0 ? grid : 1, dsa::plan::NT, dsa::plan::smem_bytes(batch),
+                                   (cudaStream_t)stream>>>(a);
+    return launch_status();
+}
+
+dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *positions, const float *inv_freq, void *out,
+                      dsa_stream_t stream) {
+    if (r == nullptr || r->n_tokens < 0 || r->n_heads < 0 || r->head_dim < 1) return DSA_ERR_INVALID_ARG;
+    if (r->rope_begin < 0 || r->rope_dim < 2 || (r->rope_dim & 1) != 0 ||
+        (int64_t)r->rope_begin + r->rope_dim > r->head_dim)
+        return DSA_ERR_INVALID_ARG;
+    if (r->layout != DSA_ROPE_HALF && r->layout != DSA_ROPE_INTERLEAVED) return DSA_ERR_INVALID_ARG;
+    if (r->dtype != DSA_ROPE_BF16 && r->dtype != DSA_ROPE_FP16 && r->dtype != DSA_ROPE_FP32) return DSA_ERR_UNSUPPORTED;
+    if (r->rope_dim > 2 * dsa::rope::MAX_PAIRS) return DSA_ERR_UNSUPPORTED;
+    if ((int64_t)r->n_heads * r->head_dim > (1 << 26)) return DSA_ERR_UNSUPPORTED;   // item counts stay in 32 bits
+    if (r->x_token_stride < 0 || r->x_head_stride < 0 || r->out_token_stride < 0 || r->out_head_stride < 0)
+        return DSA_ERR_INVALID_ARG;
+    if (!isfinite(r->scale)) return DSA_ERR_INVALID_ARG;
+    // output rows must be distinct: every dimension longer than 1 moves by at least a head
+    if ((r->n_tokens > 1 && r->out_token_stride < r->head_dim) || (r->n_heads > 1 && r->out_head_stride < r->head_dim))
+        return DSA_ERR_INVALID_ARG;
+    if (r->n_tokens == 0 || r->n_heads == 0) return DSA_OK;
+    const uintptr_t esize = r->dtype == DSA_ROPE_FP32 ? 4 : 2;
+    if (!x || !positions || !inv_freq || !out) return DSA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & (esize - 1)) != 0 ||
+        ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3u) != 0)
+        return DSA_ERR_INVALID_ARG;
+    const bool in_place = x == out;
+    if (in_place && (r->x_token_stride != r->out_token_stride || r->x_head_stride != r->out_head_stride))
+        return DSA_ERR_INVALID_ARG;
+    const bool il = r->layout == DSA_ROPE_INTERLEAVED;
+    // 16-byte vectors where every vector of every head starts on 16 bytes and none straddles
+    // the rotated part's borders (or its middle, in the half layout); single pairs otherwise
+    const int64_t v = 16 / (int64_t)esize;
+    const int64_t grain = r->rope_begin | (il ? r->rope_dim : r->rope_dim / 2) | (in_place ? 0 : r->head_dim) |
+                          (r->n_tokens > 1 ? r->x_token_stride | r->out_token_stride : 0) |
+                          (r->n_heads > 1 ? r->x_head_stride | r->out_head_stride : 0);
+    const bool vec = grain % v == 0 && aligned16(x) && aligned16(out);
+    dsa::rope::Args a{x, out, positions, inv_freq, r->n_tokens, r->n_heads, r->head_dim, r->rope_begin, r->rope_dim,
+                      r->x_token_stride, r->x_head_stride, r->out_token_stride, r->out_head_stride, r->scale,
+                      r->transposed != 0, in_place, 1};
+    // tokens per CTA: about four vectors per thread
+    const int64_t per_head = vec ? (il ? r->rope_dim : r->rope_dim / 2) / v + (in_place ? 0 : (r->head_dim - r->rope_dim) / v)
+                                 : r->rope_dim / 2 + (in_place ? 0 : r->head_dim - r->rope_dim);
+    int64_t nt = 4 * dsa::rope::NT / (per_head * r->n_heads);
+    const int64_t fit = dsa::rope::MAX_PAIRS / (r->rope_dim / 2);
+    nt = nt < fit ? nt : fit;
+    nt = nt < dsa::rope::MAX_TOKENS ? nt : dsa::rope::MAX_TOKENS;
+    a.tokens_per_cta = nt > 1 ? (int)nt : 1;
+    const unsigned grid = (unsigned)(((int64_t)r->n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta);
+    auto launch = [&](auto kernel) { kernel<<<grid, dsa::rope::NT, 0, (cudaStream_t)stream>>>(a); };
+    if (r->dtype == DSA_ROPE_FP32) {
+        if (vec) il ? launch(dsa::rope::rope_kernel<float, 4, true>) : launch(dsa::rope::rope_kernel<float, 4, false>);
+        else il ? launch(dsa::rope::rope_kernel<float, 1, true>) : launch(dsa::rope::rope_kernel<float, 1, false>);
+    } else if (r->dtype == DSA_ROPE_FP16) {
+        if (vec) il ? launch(dsa::rope::rope_kernel<__half, 8, true>) : launch(dsa::rope::rope_kernel<__half, 8, false>);
+        else il ? launch(dsa::rope::rope_kernel<__half, 1, true>) : launch(dsa::rope::rope_kernel<__half, 1, false>);
+    } else {
+        if (vec) il ? launch(dsa::rope::rope_kernel<__nv_bfloat16, 8, true>) : launch(dsa::rope::rope_kernel<__nv_bfloat16, 8, false>);
+        else il ? launch(dsa::rope::rope_kernel<__nv_bfloat16, 1, true>) : launch(dsa::rope::rope_kernel<__nv_bfloat16, 1, false>);
+    }
+    return launch_status();
+}
+
+dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, double original_len, double beta_fast,
+                                  double beta_slow, float *inv_freq, double *attention_factor) {
+    if (rope_dim < 2 || (rope_dim & 1) != 0 || !(base > 1.0) || !(factor >= 1.0) || !isfinite(base) || !isfinite(factor) ||
+        inv_freq == nullptr)
+        return DSA_ERR_INVALID_ARG;
+    const bool stretched = factor > 1.0;
+    double low = 0.0, high = 0.0;
+    if (stretched) {
+        if (!(original_len >= 1.0) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow)) return DSA_ERR_INVALID_ARG;
+        const double two_pi = 6.283185307179586;
+        low = floor(rope_dim * log(original_len / (beta_fast * two_pi)) / (2.0 * log(base)));
+        high = ceil(rope_dim * log(original_len / (beta_slow * two_pi)) / (2.0 * log(base)));
+        if (low < 0.0) low = 0.0;
+        if (high > rope_dim - 1.0) high = rope_dim - 1.0;
+    }
+    for (int i = 0; i < rope_dim / 2; ++i) {
+        const double f = pow(base, -2.0 * i / rope_dim);
+        double w = 0.0;
+        if (stretched) {
+            const double span = high - low;
+            w = (i - low) / (span > 0.001 ? span : 0.001);
+            w = w < 0.0 ? 0.0 : (w > 1.0 ? 1.0 : w);
+        }
+        inv_freq[i] = (float)(f / factor * w + f * (1.0 - w));
+    }
+    if (attention_factor != nullptr) *attention_factor = stretched ? 0.1 * log(factor) + 1.0 : 1.0;
+    return DSA_OK;
+}
+
+size_t dsa_sparse_mla_fp8_workspace_size(const dsa_problem_t *p) {
+    if (check_problem(p) != DSA_OK) return 0;
+    return mla_split_bytes(p);
+}
+
+dsa_status_t dsa_sparse_mla_fp8_fwd(const dsa_problem_t *p, const void *q, const void *kv, const void *kv_scale,
+                                    const int32_t *idx, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                    dsa_stream_t stream) {
+    dsa_status_t st = check_problem(p);
+    if (st != DSA_OK) return st;
+    if (p->total_q == 0) return DSA_OK;
+    if (!q || !kv || !kv_scale || !idx || !out || !lse) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv) || !aligned16(idx) || !aligned16(out) || !aligned16(lse)) return DSA_ERR_INVALID_ARG;
+    const size_t need = dsa_sparse_mla_fp8_workspace_size(p);
+    if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return DSA_ERR_WORKSPACE;
+    if ((st = set_smem_attrs()) != DSA_OK) return st;
+    dsa::mla8::sparse_mla_fp8_plain_kernel<<<(unsigned)p->total_q * 8u, dsa::mla8::NT, dsa::mla8::SMEM,
+                                             (cudaStream_t)stream>>>(
+        to_dev(p), reinterpret_cast<const __nv_bfloat16 *>(q), static_cast<const unsigned char *>(kv),
+        static_cast<const unsigned char *>(kv_scale), idx, reinterpret_cast<__nv_bfloat16 *>(out), lse);
     return launch_status();
 }
 

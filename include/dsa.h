@@ -276,12 +276,145 @@ dsa_status_t dsa_check_device_errors(dsa_stream_t stream);
  *   k_idx_raw : [n, 128] bf16      kv_raw : [n, 576] bf16      positions, rows : [n] int32
  *   k_norm_w, k_norm_b : [128] fp32   kv_norm_w : [512] fp32   inv_freq : [32] fp32
  *   k_idx_cache : bf16 [.., 128]   kv_cache : bf16 [.., 576]   (rows[t]: the destination
- *   row, packed or through a block table; distinct rows, no two tokens write the same row)
+ *   row, packed or through a block table; distinct rows, no two tokens write the same row;
+ *   a token with rows[t] < 0 is passed over)
  */
 dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw,
                              const int32_t *positions, const int32_t *rows, const float *k_norm_w,
                              const float *k_norm_b, const float *kv_norm_w, const float *inv_freq,
                              float eps, void *k_idx_cache, void *kv_cache, dsa_stream_t stream);
+
+/*
+ * Page plan of one step: sequence offsets, slot map and block-table entries from the
+ * requests' lengths, made on the GPU (paged caches of 64-token pages, "DeepSeek-V3.2" (miles
+ * docs) §5.3; the pages give the page size, the bookkeeping is this build's).  Request b holds
+ * len_cached[b] tokens in its pages and gets len_new[b] more (0 allowed).
+ *   cu_q  = exclusive sums of len_new, cu_k = exclusive sums of len_cached + len_new: the
+ *           offsets a dsa_problem_t takes ([batch + 1] each)
+ *   block_table [batch, max_pages], updated in place: request b keeps its
+ *           ceil(len_cached / 64) pages; the ones it needs beyond them are taken from
+ *           free_pages[head ..], in order of b and within b in order of the pages.  Entries
+ *           past a request's last page are left as they were.
+ *   positions[t], rows[t] for token t = cu_q[b] + i: len_cached[b] + i, and the cache row
+ *           page * 64 + position % 64 (what dsa_cache_write / dsa_cache_write_fp8 take).
+ *           Tokens cu_q[batch] .. n_tokens - 1 (a token axis padded for a captured graph) get
+ *           position 0 and row -1, which those calls pass over.
+ *   counts  [4]: new tokens, pages taken, longest sequence, error bits
+ * free_head (device, may be NULL = 0) is the number of free_pages already used; it is read
+ * only: the next step's head is head + counts[1].
+ * Error bits (counts[3]): 1 the free list is too short, 2 a sequence needs more than
+ * max_pages pages, 4 more new tokens than n_tokens (or more than 2^31 - 1 keys), 8 a negative
+ * length.  With any of them the step is an empty batch: cu_q = cu_k = 0, every position 0
+ * and row -1, counts[0..2] = 0, and block_table is left as it was.
+ * A page number outside 0 .. n_pages - 1 (in block_table or free_pages) gives its tokens row
+ * -1 and DSA_ERR_DEVICE_BOUNDS from dsa_check_device_errors.
+ *   1 <= batch <= 8192, n_tokens >= 0, max_pages >= 1, n_free >= 0, 1 <= n_pages < 2^25
+ *   len_cached, len_new : [batch] int32   free_pages : [n_free] int32 (NULL if n_free == 0)
+ * No array may overlap another.
+ */
+dsa_status_t dsa_paged_plan(int32_t batch, const int32_t *len_cached, const int32_t *len_new,
+                            int32_t *block_table, int32_t max_pages, const int32_t *free_pages,
+                            int32_t n_free, const int32_t *free_head, int32_t n_pages, int32_t *cu_q,
+                            int32_t *cu_k, int32_t *positions, int32_t *rows, int32_t n_tokens,
+                            int32_t *counts, dsa_stream_t stream);
+
+/* RoPE pairs of a rotated part of d dims: HALF (i, i + d / 2), INTERLEAVED (2i, 2i + 1). */
+typedef enum dsa_rope_layout { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 } dsa_rope_layout_t;
+typedef enum dsa_rope_dtype { DSA_ROPE_BF16 = 0, DSA_ROPE_FP16 = 1, DSA_ROPE_FP32 = 2 } dsa_rope_dtype_t;
+
+typedef struct dsa_rope_desc {
+    int32_t n_tokens, n_heads, head_dim;   /* x and out: [n_tokens, n_heads, head_dim] */
+    int32_t rope_begin, rope_dim;          /* rotated dims: rope_begin .. + rope_dim, even, <= 1024 */
+    dsa_rope_layout_t layout;
+    dsa_rope_dtype_t dtype;
+    int64_t x_token_stride, x_head_stride;       /* in elements; the last dimension is dense */
+    int64_t out_token_stride, out_head_stride;
+    float scale;                           /* multiplies the rotated dims (1, or an attention factor) */
+    int32_t transposed;                    /* nonzero: turn by the negative angle */
+} dsa_rope_desc_t;
+
+/*
+ * Rotary positions of the queries ("DeepSeek-V3.2-Exp" README, 2025-11-17 note: the indexer's
+ * RoPE input is non-interleaved, MLA's interleaved; dsa_cache_write rotates the keys):
+ *   (u, v) -> scale * (u cos a - v sin a, v cos a + u sin a),  a = positions[t] * inv_freq[i]
+ * for each pair i of the rotated dims; the angle, its cosine and sine are evaluated in fp64,
+ * the rotation in fp32, and the result is rounded once to the tensor's type.  The other dims
+ * of a head are copied.  out == x with the same strides rotates in place; any other overlap
+ * of x and out is not allowed.  transposed != 0 applies the transposed map: the gradient of x
+ * from the gradient of out on the rotated dims (copied dims pass through).
+ *   positions : [n_tokens] int32      inv_freq : [rope_dim / 2] fp32
+ * Pointers need the alignment of their element type only (16-byte aligned slices and
+ * strides are faster); strides >= 0; |scale| finite.
+ */
+dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *positions,
+                      const float *inv_freq, void *out, dsa_stream_t stream);
+
+/*
+ * RoPE frequencies of rope_dim rotated dims, on the HOST (no device work): inv_freq[i] =
+ * base^(-2i / rope_dim), and, where factor > 1, stretched for long contexts by the YaRN rule
+ * ("Model techniques map -- DeepSeek-V3.2", rope scaling: base 10000, factor 40, original
+ * length 4096, beta_fast 32, beta_slow 1, 163,840 positions): with r(n) = rope_dim *
+ * ln(original_len / (2 pi n)) / (2 ln base), low = floor(r(beta_fast)) clipped to >= 0,
+ * high = ceil(r(beta_slow)) clipped to <= rope_dim - 1 and w_i = clip((i - low) /
+ * max(high - low, 0.001), 0, 1):   inv_freq[i] = base^(-2i / rope_dim) * (w_i / factor + 1 - w_i).
+ *   inv_freq : host [rope_dim / 2] fp32
+ *   attention_factor : host, may be NULL: 0.1 * ln(factor) + 1 for factor > 1, else 1
+ * DSA_ERR_INVALID_ARG for a NULL array, an odd or non-positive rope_dim, base <= 1,
+ * factor < 1, original_len < 1 (with factor > 1), beta_fast < beta_slow or beta_slow <= 0.
+ */
+dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, double original_len,
+                                  double beta_fast, double beta_slow, float *inv_freq,
+                                  double *attention_factor);
+
+/*
+ * Key-cache write in 8 bits: dsa_cache_write's rows, quantised.  With k = the indexer key and
+ * lat [512], rot [64] = the latent's two parts as defined there, and Q = rounding to the
+ * nearest e4m3 number (ties to even):
+ *   indexer key, by idx_dtype (the forms dsa_indexer_scores takes):
+ *     DSA_BF16        k_idx_cache bf16 [.., 128]; k_scale_cache NULL
+ *     DSA_E4M3        codes Q(k / s), s = max|k| / 448 (1 for a zero row); k_scale_cache fp32 [..]
+ *     DSA_E4M3_UE8M0  codes Q(k / s), s the smallest power of two with max|k| <= 448 s;
+ *                     k_scale_cache uint8 [..] ue8m0
+ *   latent row, 640 codes and one ue8m0 scale s, the smallest power of two with
+ *   |lat| <= 448 s and |rot| <= 16 * 448 s:
+ *     kv_cache[row, 0:512] = Q(lat / s)
+ *     kv_cache[row, 512:576] = hi = Q(rot / (16 s)),  kv_cache[row, 576:640] = Q(rot / (16 s) - hi)
+ *   so the row stands for the latent code * s and the RoPE dims (hi + lo) * 16 s.  Every
+ *   element keeps 4 significant bits (RoPE dims: 8) down to 2^-15 of the largest one.
+ * Power-of-two scales are at least 2^-126.  Arithmetic up to the code in fp64: each code is
+ * the nearest one to the exact value.  A row that holds an infinity or a NaN gets the scale
+ * NaN (0xFF) and NaN codes.  Tokens with rows[t] < 0 are passed over; other rows are left as
+ * they were.
+ *   kv_cache : uint8 [.., 640]   kv_scale_cache : uint8 [..]     other tensors as dsa_cache_write
+ *   (kv_scale_cache and a uint8 k_scale_cache need no alignment)
+ */
+dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw,
+                                 const int32_t *positions, const int32_t *rows, const float *k_norm_w,
+                                 const float *k_norm_b, const float *kv_norm_w, const float *inv_freq,
+                                 float eps, dsa_dtype_t idx_dtype, void *k_idx_cache, void *k_scale_cache,
+                                 void *kv_cache, void *kv_scale_cache, dsa_stream_t stream);
+
+/*
+ * dsa_sparse_mla_fwd over the 8-bit latent cache of dsa_cache_write_fp8: the same z, out and
+ * lse with kv[s, :] the values the row's codes stand for; the same rules for slots that are
+ * negative, in the future or out of range, for repeated indices and for rows without a valid
+ * slot (out = 0, lse = -inf).  Query rows behind the last sequence (t >= cu_q[B]) count as
+ * rows without a valid slot.  What a masked slot's cache row holds (NaN included) has no
+ * effect.
+ * Accuracy: q and the probabilities enter the tensor cores as two e4m3 numbers each (8
+ * significant bits), products are exact and sums are fp32.  A probability is held relative to
+ * the largest scale among the keys its row has read so far: next to keys whose scale is 2^n
+ * times its own, a key keeps 2^-16 of the largest probability's weight times 2^n.
+ *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd
+ *   workspace : device, >= dsa_sparse_mla_fp8_workspace_size(p) bytes, 256-byte aligned (may
+ *               be NULL when that is 0).  It holds the parts of rows that are split over
+ *               several SM pairs when there are few query rows: calls that share it must not
+ *               overlap on the GPU (two captured graphs replayed at once need one each).
+ */
+size_t dsa_sparse_mla_fp8_workspace_size(const dsa_problem_t *p);
+dsa_status_t dsa_sparse_mla_fp8_fwd(const dsa_problem_t *p, const void *q, const void *kv,
+                                    const void *kv_scale, const int32_t *idx, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, dsa_stream_t stream);
 
 /*
  * Self-test of the device-side failure path (no counterpart on the pages): launches one
