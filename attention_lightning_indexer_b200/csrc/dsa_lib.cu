@@ -147,8 +147,11 @@ dsa_status_t set_smem_attrs() {
         e = cudaFuncSetAttribute(dsa::mla::sparse_mla_pair_kernel<false, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, dsa::mla::PairCfg::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dsa::mla8::sparse_mla_fp8_plain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dsa::mla8::SMEM);
+        e = cudaFuncSetAttribute(dsa::mla8::sparse_mla_fp8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dsa::mla8::Cfg::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dsa::mla8::sparse_mla_fp8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dsa::mla8::Cfg::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(dsa::plan::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)dsa::plan::smem_bytes(dsa::plan::MAX_BATCH));
@@ -265,26 +268,31 @@ size_t mla_split_bytes(const dsa_problem_t *p) {
     return align_up((size_t)p->total_q * (size_t)ns * 128 * 513 * sizeof(float), 256);
 }
 
-// CTA pairs of one attention instantiation that run at once on the current device (one
-// CTA per SM; asked of the occupancy calculator once per device, after the shared-memory
-// attribute is set).
-template <bool DENSE, bool SPLIT>
-int mla_resident_pairs() {
+// CTA pairs of one attention kernel that run at once on the current device (one CTA per SM;
+// asked of the occupancy calculator once per device, after the shared-memory attribute is
+// set).
+template <auto KERNEL, int THREADS, int SMEM>
+int resident_pairs() {
     static int pairs[MAX_DEVICES] = {};
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
     if (pairs[dev] > 0) return pairs[dev];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(dsa::mla::PairCfg::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = dsa::mla::PairCfg::SMEM;
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, dsa::mla::sparse_mla_pair_kernel<DENSE, SPLIT>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
     pairs[dev] = n;
     return n;
+}
+
+template <bool DENSE, bool SPLIT>
+int mla_resident_pairs() {
+    return resident_pairs<dsa::mla::sparse_mla_pair_kernel<DENSE, SPLIT>, dsa::mla::PairCfg::THREADS, dsa::mla::PairCfg::SMEM>();
 }
 
 dsa_status_t mla_launch(const dsa_problem_t *p, const void *q, const void *kv, const int32_t *idx, void *out,
@@ -329,6 +337,38 @@ dsa_status_t mla_launch(const dsa_problem_t *p, const void *q, const void *kv, c
     if (st != DSA_OK || sp.nsplit < 2) return st;
     dsa::mla::combine_splits_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part,
                                                                                    sp.lse_part, ob, lse);
+    return launch_status();
+}
+// The attention over the 8-bit cache; split_ws holds the parts of split rows (mla_split_plan).
+dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *kv, const void *kv_scale, const int32_t *idx,
+                            void *out, float *lse, cudaStream_t stream, void *split_ws) {
+    using C = dsa::mla8::Cfg;
+    dsa::mla::SplitArgs sp{1, 1 << 22, nullptr, nullptr};
+    mla_split_plan(p, &sp.nsplit, &sp.bps);
+    if (sp.nsplit > 1) {
+        sp.o_part = static_cast<float *>(split_ws);
+        sp.lse_part = sp.o_part + (size_t)p->total_q * (size_t)sp.nsplit * 128 * 512;
+    }
+    CUtensorMap tq, tkv;
+    // q: [T*128 rows, 576] read as 64-row boxes of 64 dims; kv: [S rows, 640 codes] gathered 4 rows
+    // x 128 codes at a time (one-row boxes)
+    if (!make_tmap_rows(&tq, q, false, 576, (uint64_t)p->total_q * 128, 64)) return DSA_ERR_CUDA;
+    if (!make_tmap_rows(&tkv, kv, true, dsa::cache::KV8_CODES, (uint64_t)(p->total_k > 0 ? p->total_k : 1), 1))
+        return DSA_ERR_CUDA;
+    const long long units = (long long)p->total_q * sp.nsplit;
+    const int resident = sp.nsplit > 1 ? resident_pairs<dsa::mla8::sparse_mla_fp8_kernel<true>, C::THREADS, C::SMEM>()
+                                       : resident_pairs<dsa::mla8::sparse_mla_fp8_kernel<false>, C::THREADS, C::SMEM>();
+    if (resident <= 0) return DSA_ERR_CUDA;
+    const unsigned grid = 2u * (unsigned)(units < resident ? units : resident);
+    auto *ob = reinterpret_cast<__nv_bfloat16 *>(out);
+    const auto *sc = static_cast<const unsigned char *>(kv_scale);
+    if (sp.nsplit > 1)
+        dsa::mla8::sparse_mla_fp8_kernel<true><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, ob, lse, sp);
+    else
+        dsa::mla8::sparse_mla_fp8_kernel<false><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, ob, lse, sp);
+    dsa_status_t st = launch_status();
+    if (st != DSA_OK || sp.nsplit < 2) return st;
+    dsa::mla::combine_splits_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
     return launch_status();
 }
 
@@ -827,11 +867,7 @@ dsa_status_t dsa_sparse_mla_fp8_fwd(const dsa_problem_t *p, const void *q, const
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
         return DSA_ERR_WORKSPACE;
     if ((st = set_smem_attrs()) != DSA_OK) return st;
-    dsa::mla8::sparse_mla_fp8_plain_kernel<<<(unsigned)p->total_q * 8u, dsa::mla8::NT, dsa::mla8::SMEM,
-                                             (cudaStream_t)stream>>>(
-        to_dev(p), reinterpret_cast<const __nv_bfloat16 *>(q), static_cast<const unsigned char *>(kv),
-        static_cast<const unsigned char *>(kv_scale), idx, reinterpret_cast<__nv_bfloat16 *>(out), lse);
-    return launch_status();
+    return mla_fp8_launch(p, q, kv, kv_scale, idx, out, lse, (cudaStream_t)stream, workspace);
 }
 
 dsa_status_t dsa_selftest_bounded_wait(uint32_t limit_us, dsa_stream_t stream) {

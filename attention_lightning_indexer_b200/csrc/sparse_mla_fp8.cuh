@@ -1,95 +1,879 @@
 // sparse_mla_fp8.cuh -- attention over the selected rows of the 8-bit latent cache
-// (cache_write_fp8.cuh gives the row format): MLA in MQA mode, 128 heads, 576-d rows, the
-// value is the 512-d latent.
+// (cache_write_fp8.cuh gives the row format) on pairs of SMs: MLA in MQA mode, 128 heads over
+// 576-d rows, the value is the 512-d latent.
 //   z[t,h,i] = sm_scale * q[t,h,:] . kv[idx[t,i], :]     out = softmax(z) . kv[:, 0:512]
-// Plain form: one CTA per (token, 16 heads), 32 keys at a time dequantised into shared
-// memory, running maximum and sum per head.
+//
+// Eight bits on the tensor cores without losing the other operand's: a bf16 number has 8
+// significant bits and e4m3 has 4, so q (and a probability) is the sum of two e4m3 numbers,
+// hi = Q(x) and lo = Q(x - hi), and every product with a cached code is two kind::f8f6f4
+// MMAs, each at twice the bf16 rate: the tensor time of the bf16 form, but the cached rows go
+// from HBM into the MMA as they are.  Nothing is dequantised, the gathers move 144 KB per CTA and
+// block instead of 272 KB, and a ring slot holds 128 dims of a key instead of 64.
+//
+// The row's scale 2^e leaves the sums: S^T[key, h] is over codes, and its thread (which owns
+// one key) multiplies by 2^e; for the values, the probability takes the scale with it, P' =
+// p 2^(e - er + BASE), er the largest scale exponent among the keys this unit has read so far.
+// The RoPE dims are in the row as two codes of 64 dims at 16 times the row's scale, so q's
+// RoPE dims are taken 16 times: the K axis is 4 atoms of latent codes and one atom [hi | lo],
+// multiplied by the same 64 RoPE dims of q twice.
+//
+// The schedule is that of the bf16 kernel (sparse_mla_pair.cuh): persistent CTA pairs take
+// (token, split) units in turn; blocks of 256 index slots, CTA c owns slots 128 c .. + 127 of
+// each block and heads 64 c .. + 63;
+//   QK_b   S^T[key, h], M = 256 keys (A: the gathered atoms of each CTA's own keys, K-major),
+//          N = 128 heads (B: q hi / lo, 64 heads per CTA), K = 640 codes: 40 MMAs of K = 32
+//   PV_b   O^T[d, h] += codes^T P'^T, M = 256 value dims twice (A: CTA c holds dims 256 i +
+//          128 c .. + 127 of all 256 keys, MN-major), N = 128 heads (B: P'^T hi / lo, MN-major,
+//          heads 64 c .. + 63 in CTA c), K = 256 keys: 32 MMAs
+// with a 7-slot ring of 16 KB atoms (128 keys x 128 codes, tile::gather4, 128-byte swizzle) in
+// MMA order QK_0, QK_1, PV_0, QK_2, PV_1, ...: five atoms for QK_b, four for PV_b (i = 0, 1 and
+// key half h = 0, 1).  A masked slot gathers a visible row of its token, so what lies in other
+// rows never enters a sum.
+//
+// Probabilities: the reference maximum m[h] moves when a block maximum exceeds it by more than
+// TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and its smallest step 2^-9 is 2^-15 of the
+// largest p.  The sum l takes p itself in fp32.
+//
+// Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
+// prepare (warp 8 also publishes each unit's block count and loads its q: the raw bf16 rows
+// land in q_s and are split in place into hi and lo, each head at its own power of two; then
+// they fetch the scales of the keys of each block, up to four blocks ahead), 12-19 softmax and
+// epilogue: TMEM lane quarter w % 4, head half (w - 12) / 4.
 #pragma once
 
 #include "cache_write_fp8.cuh"
 #include "dsa_common.cuh"
+#include "sm100.cuh"
 #include "sparse_mla_pair.cuh"
 
 namespace dsa {
 namespace mla8 {
 
-constexpr int NT = 256, HG = 16, KC = 32, KVP = 577;
-constexpr int SMEM = (HG * 576 + KC * KVP + HG * KC + 3 * HG + KC) * 4;
+struct Cfg {
+    static constexpr int BLK = 256;                 // index slots per block (128 per CTA)
+    static constexpr int ATOM = 128 * 128;          // one gathered atom: 128 keys x 128 codes
+    static constexpr int QK_ATOMS = 5, PV_ATOMS = 4;
+    static constexpr int QATOM = 64 * 128;          // 64 heads x 128 bytes
+    static constexpr int NQ = 9;                    // raw: 9 x 64 dims; split: 4 hi, 4 lo, [RoPE hi | lo]
+    static constexpr int NSLOT = 7, NLOAD = 7;
+    static constexpr int NINFO = 4;                 // blocks of key scales kept ahead
+    static constexpr int NQS = 4;                   // units of q scales kept
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_PH = OFF_Q + NQ * QATOM;           // P' hi [256 keys][64 heads]
+    static constexpr int OFF_PL = OFF_PH + 256 * 64;            // P' lo
+    static constexpr int OFF_RING = OFF_PL + 256 * 64;
+    static constexpr int OFF_RED = OFF_RING + NSLOT * ATOM;     // [4][128] f32
+    static constexpr int OFF_XM = OFF_RED + 4 * 128 * 4;        // [2][128] f32, peer block maxima
+    static constexpr int OFF_XL = OFF_XM + 2 * 128 * 4;         // [128] f32, peer row sums
+    static constexpr int OFF_MR = OFF_XL + 128 * 4;             // [128] f32, reference maxima
+    static constexpr int OFF_FS = OFF_MR + 128 * 4;             // [128] f32, rescale factor / output factor
+    static constexpr int OFF_QS = OFF_FS + 128 * 4;             // [NQS][128] f32, 2^f[h] * sm_scale * log2 e
+    static constexpr int OFF_INFO = OFF_QS + NQS * 128 * 4;     // [NINFO][128] f32, key scale or -1 (masked)
+    static constexpr int OFF_ER = OFF_INFO + NINFO * 128 * 4;   // [NINFO][4] int, running maxima of exponents
+    static constexpr int OFF_BAR = OFF_ER + NINFO * 4 * 4;
+    // empty[7] pfull[7] q_raw q_ready q_free s_full[2] s_free[2] p_full pv_done o_ready xbar[2] lbar
+    // drain unit_full[2] unit_free[2] info_full[4] info_free[4]
+    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO;
+    // [0] TMEM base, [1] abort, [2..3] unit blocks, [4..5] unit fallback keys, [6] peer's abort flag
+    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
+    static constexpr int OFF_LASTPOS = OFF_MISC + 32;           // even CTA: [2][NSLOT] last ring position issued
+    static constexpr int SMEM = OFF_LASTPOS + 2 * NSLOT * 4;
+    static constexpr int PREP0 = 8, SOFT0 = 12, WARPS = 20, THREADS = 32 * WARPS;
+    // of the 640 x 96 registers of the launch: 256 x 56 + 128 x 72 + 256 x 144 = 60,416
+    static constexpr int REG_LOAD = 56, REG_PREP = 72, REG_SOFT = 144;
+    static constexpr int TMEM_S = 0, TMEM_O = 256;
+    static constexpr float TAU = 2.8f;              // lazy-rescale threshold (log2 units)
+    static constexpr int BASE = 6;                  // 2^(TAU + BASE) = 446 < 448
+    static constexpr int ER_MIN = BASE;             // exponent bytes below this count as this
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(NLOAD == NSLOT, "one ring slot per gathering warp");
+    static_assert(256 * REG_LOAD + 128 * REG_PREP + 256 * REG_SOFT <= 640 * 96, "register split");
+};
 
-__global__ void __launch_bounds__(NT)
-sparse_mla_fp8_plain_kernel(Problem P, const __nv_bfloat16 *__restrict__ q, const unsigned char *__restrict__ kv,
-                            const unsigned char *__restrict__ kv_scale, const int32_t *__restrict__ idx,
-                            __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    extern __shared__ float sm[];
-    float *qs = sm, *ks = qs + HG * 576, *ps = ks + KC * KVP, *ms = ps + HG * KC, *ls = ms + HG, *fs = ls + HG;
-    int *vis = reinterpret_cast<int *>(fs + HG);
-    const int t = blockIdx.x >> 3, h0 = (blockIdx.x & 7) * HG, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const RowInfo ri = row_info(P, t);
-    const bool row_live = row_ok(P, ri) && ri.pos < ri.len_k;
-    for (int i = tid; i < HG * 576; i += NT) qs[i] = __bfloat162float(q[((int64_t)t * 128 + h0) * 576 + i]) * P.sm_scale;
-    if (tid < HG) {
-        ms[tid] = -INFINITY;
-        ls[tid] = 0.f;
+// 2-SM MMA of e4m3 operands (see sm100::mma_f16_pair).
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// MN-major operand in the 64-byte swizzle: rows of 64 bytes along MN, 8-row (512-byte) groups
+// along K, 16-byte chunk c of row r at chunk c ^ ((r >> 1) & 3) (layout 4 = SW64).
+__device__ __forceinline__ uint64_t desc_sw64_mn(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(512 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;
+    return d;
+}
+
+// Maximum over the warp of v (NaN passed over), in every lane.
+__device__ __forceinline__ float warp_fmax(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Two fp16 numbers as hi = Q(x) and lo = Q(x - hi) (two e4m3 codes each).
+__device__ __forceinline__ void split_e4m3(__half2 x, uint32_t &hi, uint32_t &lo) {
+    const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
+    hi = h;
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
+}
+
+struct Unit {
+    int nblocks;
+    int fallback;   // a visible key of the token (position within its sequence)
+};
+
+// Blocks of one unit (token row ri, blocks split * bps ..) up to the last visible slot of the
+// index row, and that slot's key (the same in every lane of the warp).
+__device__ __forceinline__ Unit unit_scan(const Problem &P, const RowInfo &ri, const int32_t *irow, int K, int split,
+                                          int bps, int lane) {
+    Unit u{0, 0};
+    if (ri.pos >= ri.len_k || !row_ok(P, ri)) return u;   // behind the last sequence, or a bad row
+    int last = -1;
+    if ((K & 3) == 0) {
+        const int n4 = K >> 2;
+#pragma unroll 4
+        for (int i4 = lane; i4 < n4; i4 += 32) {
+            const int4 x = __ldg(reinterpret_cast<const int4 *>(irow) + i4);
+            if (mla::pair_visible(x.x, ri)) last = 4 * i4;
+            if (mla::pair_visible(x.y, ri)) last = 4 * i4 + 1;
+            if (mla::pair_visible(x.z, ri)) last = 4 * i4 + 2;
+            if (mla::pair_visible(x.w, ri)) last = 4 * i4 + 3;
+        }
+    } else {
+        for (int i = lane; i < K; i += 32)
+            if (mla::pair_visible(__ldg(irow + i), ri)) last = i;
     }
-    float acc[HG][2] = {};
-    for (int k0 = 0; k0 < P.topk && row_live; k0 += KC) {
-        __syncthreads();
-        if (tid < KC) {
-            const int e = k0 + tid < P.topk ? idx[(int64_t)t * P.topk + k0 + tid] : -1;
-            vis[tid] = mla::pair_visible(e, ri) ? key_row(P, ri, e) : -1;
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (last < 0) return u;
+    const int nb_row = (last + Cfg::BLK) / Cfg::BLK;
+    const int b_begin = split * bps;
+    u.nblocks = max(0, min(nb_row, b_begin + bps) - b_begin);
+    u.fallback = __ldg(irow + last);
+    return u;
+}
+
+template <bool SPLIT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, Problem P,
+                      const unsigned char *__restrict__ kv_scale, const int32_t *__restrict__ idx,
+                      __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, mla::SplitArgs sp) {
+    using C = Cfg;
+    using namespace sm100;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cr = (int)cluster_ctarank();                   // 0: issues the MMAs
+    const int peer = cr ^ 1;
+    const int T = P.total_q, K = P.topk;
+    const int nsplit = SPLIT ? sp.nsplit : 1;
+    const int bps = SPLIT ? sp.bps : (1 << 22);
+    const int units = T * nsplit;
+    const int npairs = (int)(gridDim.x >> 1);
+    const int pair0 = (int)(blockIdx.x >> 1);
+
+    const uint32_t sbase = smem_u32(smem);
+    const bool misaligned = (sbase & 1023u) != 0;           // uniform; no unit runs then
+    const uint32_t q_s = sbase + C::OFF_Q;
+    const uint32_t ph_s = sbase + C::OFF_PH, pl_s = sbase + C::OFF_PL;
+    const uint32_t ring_s = sbase + C::OFF_RING;
+    float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
+    float *xm = reinterpret_cast<float *>(smem + C::OFF_XM);
+    float *xl = reinterpret_cast<float *>(smem + C::OFF_XL);
+    float *mr = reinterpret_cast<float *>(smem + C::OFF_MR);
+    float *fs = reinterpret_cast<float *>(smem + C::OFF_FS);
+    float *qsc = reinterpret_cast<float *>(smem + C::OFF_QS);
+    float *info = reinterpret_cast<float *>(smem + C::OFF_INFO);
+    int *ers = reinterpret_cast<int *>(smem + C::OFF_ER);
+    const uint32_t bar0 = sbase + C::OFF_BAR;
+    auto empty = [&](int s) { return bar0 + 8u * s; };
+    auto pfull = [&](int s) { return bar0 + 8u * (C::NSLOT + s); };
+    const uint32_t q_raw = bar0 + 8u * (2 * C::NSLOT);       // this CTA's raw q landed
+    const uint32_t q_ready = q_raw + 8;                      // even CTA: q of both CTAs split
+    const uint32_t q_free = q_raw + 16;                      // the unit's last QK has read q_s
+    auto s_full = [&](int b) { return q_raw + 24 + 8u * b; };
+    auto s_free = [&](int b) { return q_raw + 40 + 8u * b; };
+    const uint32_t p_full = q_raw + 56;                      // P'^T of both CTAs written (even CTA)
+    const uint32_t pv_done = q_raw + 64;
+    const uint32_t o_ready = q_raw + 72;
+    auto xbar = [&](int b) { return q_raw + 80 + 8u * b; };
+    const uint32_t lbar = q_raw + 96;
+    const uint32_t drain = q_raw + 104;
+    auto unit_full = [&](int i) { return q_raw + 112 + 8u * i; };
+    auto unit_free = [&](int i) { return q_raw + 128 + 8u * i; };
+    auto info_full = [&](int i) { return q_raw + 144 + 8u * i; };
+    auto info_free = [&](int i) { return q_raw + 144 + 8u * (C::NINFO + i); };
+    volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
+    volatile int *unit_nb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
+    volatile int *unit_fb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);
+
+    // ---- setup (every thread of both CTAs reaches the cluster barriers below)
+    if (tid == 0 && !misaligned) {
+        for (int s = 0; s < C::NSLOT; ++s) {
+            mbar_init(empty(s), 1);
+            mbar_init(pfull(s), 1);       // the even CTA's expect-tx for both CTAs' bytes
         }
-        __syncthreads();
-        for (int i = tid; i < KC * 576; i += NT) {
-            const int k = i / 576, d = i - k * 576;
-            float v = 0.f;
-            if (vis[k] >= 0) {
-                const unsigned char *r = kv + (int64_t)vis[k] * cache::KV8_CODES;
-                const float s = ue8m0_to_float(kv_scale[vis[k]]);
-                v = d < 512 ? cache::e4m3_value(r[d]) * s
-                            : (cache::e4m3_value(r[d]) + cache::e4m3_value(r[d + 64])) * cache::KV8_ROPE_GAIN * s;
-            }
-            ks[k * KVP + d] = v;
+        mbar_init(q_raw, 1);
+        mbar_init(q_ready, 8);            // 4 preparing warps of each CTA
+        mbar_init(q_free, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(s_full(b), 2);      // the MMA thread's own arrival and its commit
+            mbar_init(s_free(b), 16);     // 8 softmax warps of each CTA
+            mbar_init(xbar(b), 1);
+            mbar_init(unit_full(b), 1);   // warp 8
+            mbar_init(unit_free(b), C::NLOAD + 3 + 1 + (cr == 0 ? 1 : 0));
         }
-        __syncthreads();
-        for (int h = warp; h < HG; h += NT / 32) {
-            float z = 0.f;
-            for (int d = 0; d < 576; ++d) z = fmaf(qs[h * 576 + d], ks[lane * KVP + d], z);
-            if (vis[lane] < 0) z = -INFINITY;
-            float m = z;
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float mo = ms[h], mn = fmaxf(mo, m);
-            const float p = vis[lane] < 0 ? 0.f : expf(z - mn);
-            float l = p;
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            ps[h * KC + lane] = p;
-            __syncwarp();
-            if (lane == 0) {
-                fs[h] = mo == -INFINITY ? 0.f : expf(mo - mn);
-                ls[h] = ls[h] * fs[h] + l;
-                ms[h] = mn;
-            }
+        mbar_init(p_full, 16);            // 8 softmax warps of each CTA
+        mbar_init(pv_done, 1);
+        mbar_init(o_ready, 1);
+        mbar_init(lbar, 1);
+        mbar_init(drain, 1);
+        for (int i = 0; i < C::NINFO; ++i) {
+            mbar_init(info_full(i), 4);
+            mbar_init(info_free(i), 8);
         }
-        __syncthreads();
-        for (int h = 0; h < HG; ++h) {
-            acc[h][0] *= fs[h];
-            acc[h][1] *= fs[h];
-        }
-        for (int k = 0; k < KC; ++k) {
-            const float v0 = ks[k * KVP + tid], v1 = ks[k * KVP + tid + 256];
-            for (int h = 0; h < HG; ++h) {
-                acc[h][0] = fmaf(ps[h * KC + k], v0, acc[h][0]);
-                acc[h][1] = fmaf(ps[h * KC + k], v1, acc[h][1]);
-            }
-        }
+        misc[1] = 0;
+        misc[6] = 0;
+        for (int i = 0; i < 2 * C::NSLOT; ++i) reinterpret_cast<int *>(smem + C::OFF_LASTPOS)[i] = -1;
+        fence_barrier_init();
     }
+    if (tid == 0 && misaligned) {
+        raise_error(ERR_SMEM_ALIGN);
+        misc[1] = 1;
+    }
+    cluster_sync();   // both CTAs running, their barriers initialised
+    if (warp == 0) tmem_alloc_pair(sbase + C::OFF_MISC, 512);
+    tc_fence_before();
     __syncthreads();
-    for (int h = 0; h < HG; ++h) {
-        const float inv = ls[h] == 0.f ? 0.f : 1.0f / ls[h];
-        __nv_bfloat16 *o = out + ((int64_t)t * 128 + h0 + h) * 512;
-        o[tid] = __float2bfloat16_rn(acc[h][0] * inv);
-        o[tid + 256] = __float2bfloat16_rn(acc[h][1] * inv);
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const bool run = !misaligned;
+    const uint32_t peer_misc1 = mapa_shared(sbase + C::OFF_MISC + 4, (uint32_t)peer);
+    auto abort_pair = [&]() {                                // stop both CTAs of the pair
+        misc[1] = 1;
+        st_cluster_u32(peer_misc1, 1u);
+    };
+
+    if (warp < C::PREP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOAD));
+    if (warp < C::NLOAD) {
+        // ------------------------------------------------ gathers (one ring slot per warp)
+        const int lw = warp;
+        const uint32_t lead_pfull = mapa_shared(pfull(lw), 0);
+        const uint32_t slot_s = ring_s + lw * C::ATOM;
+        if (lw == 0 && lane == 0) prefetch_tmap(&tm_kv);
+        bool ok = run;
+        int p = 0;                                           // ring position, counted across units
+        int last_issued = -1;
+        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
+            const int t = T - 1 - u / nsplit;
+            const int split = u % nsplit;
+            const RowInfo ri = row_info_warp(P, t);
+            const bool got = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+            const int nblocks = got ? unit_nb[j & 1] : 0;
+            const int fb = got ? unit_fb[j & 1] : 0;
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) mbar_arrive(unit_free(j & 1));
+            if (nblocks == 0) continue;
+            // All atoms of a group gather the same rows; each lane loads the index entries of the
+            // next group while the current one is issued.
+            const int32_t *irow_s = idx + (int64_t)t * K + split * bps * C::BLK;
+            const int ks_left = K - split * bps * C::BLK;
+            auto entries = [&](int b, int h) {               // raw entries of this lane's 4 slots
+                const int s0 = C::BLK * b + 128 * h + 4 * lane;
+                int4 x;
+                if ((K & 3) == 0 && s0 + 3 < ks_left) {
+                    x = __ldg(reinterpret_cast<const int4 *>(irow_s + s0));
+                } else {
+                    x.x = s0 < ks_left ? __ldg(irow_s + s0) : -1;
+                    x.y = s0 + 1 < ks_left ? __ldg(irow_s + s0 + 1) : -1;
+                    x.z = s0 + 2 < ks_left ? __ldg(irow_s + s0 + 2) : -1;
+                    x.w = s0 + 3 < ks_left ? __ldg(irow_s + s0 + 3) : -1;
+                }
+                return x;
+            };
+            auto row_of = [&](int e) { return key_row(P, ri, mla::pair_visible(e, ri) ? e : fb); };
+            // group g needs key half cr of block b (QK_b, kept in e0) or both halves (PV_b)
+            int4 e0 = entries(0, cr), e1 = make_int4(-1, -1, -1, -1);
+            for (int g = 0; ok && g < 2 * nblocks; ++g) {
+                bool qk;
+                int b;
+                mla::pair_group(g, nblocks, qk, b);
+                int4 n0 = e0, n1 = e1;
+                if (g + 1 < 2 * nblocks) {
+                    bool qk1;
+                    int b1;
+                    mla::pair_group(g + 1, nblocks, qk1, b1);
+                    n0 = entries(b1, qk1 ? cr : 0);
+                    if (!qk1) n1 = entries(b1, 1);
+                }
+                const int natoms = qk ? C::QK_ATOMS : C::PV_ATOMS;
+                for (int m = 0; m < natoms; ++m) {
+                    const int pp = p + m;
+                    if (pp % C::NLOAD != lw) continue;
+                    const int4 x = (!qk && (m & 1)) ? e1 : e0;
+                    const int a = qk ? m : (m & 2) + cr;     // PV: instruction i = m >> 1, key half m & 1
+                    const int r0 = row_of(x.x), r1 = row_of(x.y), r2 = row_of(x.z), r3 = row_of(x.w);
+                    bool okw = true;
+                    if (lane == 0) {
+                        if (pp >= C::NSLOT) okw = mbar_wait(empty(lw), ((pp / C::NSLOT) - 1) & 1);
+                        if (okw && cr == 0) mbar_expect_tx(pfull(lw), 2 * C::ATOM);   // both CTAs' rows
+                    }
+                    if (!__shfl_sync(0xffffffffu, okw, 0) || misc[1]) {
+                        ok = false;
+                        break;
+                    }
+                    tma_gather4_pair(slot_s + 512 * lane, &tm_kv, lead_pfull, 128 * a, r0, r1, r2, r3);
+                    last_issued = pp;
+                }
+                e0 = n0;
+                e1 = n1;
+                p += natoms;
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) abort_pair();
+        // the last position issued into this warp's slot, recorded in the even CTA for the drain
+        // after an abort
+        if (lane == 0)
+            st_cluster_u32(mapa_shared(sbase + C::OFF_LASTPOS + 4u * (uint32_t)(cr * C::NSLOT + lw), 0),
+                           (uint32_t)last_issued);
+    } else if (lane == 0 && cr == 0) {
+        // ------------------------------------------------ MMA issuer (even CTA)
+        const uint32_t idesc_qk = idesc_e4m3(256, 128);
+        const uint32_t idesc_pv = idesc_e4m3(256, 128) | (1u << 15) | (1u << 16);   // A and B MN-major
+        const uint32_t s_full_own = mapa_shared(s_full(0), 0), s_full_peer = mapa_shared(s_full(0), 1);
+        bool ok = run;
+        bool issued = false;
+        int pos = 0;                                         // ring position, counted across units
+        int gb0 = 0;                                         // blocks of the earlier units
+        int nq = 0;                                          // units with blocks so far
+        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
+            if (!mbar_wait(unit_full(j & 1), (j >> 1) & 1)) {
+                ok = false;
+                break;
+            }
+            const int nblocks = unit_nb[j & 1];
+            mbar_arrive(unit_free(j & 1));
+            if (nblocks == 0) continue;
+            if (!mbar_wait_cluster(q_ready, nq & 1) || misc[1]) {
+                ok = false;
+                break;
+            }
+            for (int g = 0; ok && g < 2 * nblocks; ++g) {
+                bool qk;
+                int b;
+                mla::pair_group(g, nblocks, qk, b);
+                const int gb = gb0 + b;
+                if (qk) {                                    // QK_b -> S^T buffer gb & 1
+                    if (gb >= 2 && !mbar_wait_cluster(s_free(gb & 1), ((gb >> 1) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + C::TMEM_S + 128 * (gb & 1);
+                    for (int a = 0; a < C::QK_ATOMS; ++a, ++pos) {
+                        const int slot = pos % C::NSLOT;
+                        if (!mbar_wait_cluster(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sa = ring_s + slot * C::ATOM;
+                        // q: hi and lo atoms of the same 128 dims; for the RoPE atom [hi | lo] of the
+                        // keys, 64 dims of q hi and lo twice
+                        const bool rope = a == C::QK_ATOMS - 1;
+                        const uint32_t qh = q_s + (rope ? 8 : a) * C::QATOM;
+                        const uint32_t ql = rope ? qh + 64 : q_s + (4 + a) * C::QATOM;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t qo = 32u * (rope ? (kk & 1) : kk);
+                            const uint64_t da = desc_sw128(sa + kk * 32);
+                            mma_f8_pair(d, da, desc_sw128(qh + qo), idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
+                            mma_f8_pair(d, da, desc_sw128(ql + qo), idesc_qk, 1u);
+                        }
+                        issued = true;
+                        mma_commit_pair_both(empty(slot));
+                    }
+                    if (!ok) break;
+                    if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
+                    // this thread's own arrivals pass on what it has seen (the q scales, through
+                    // q_ready) to the softmax warps that wait for S^T
+                    mbar_arrive_cluster(s_full_own + 8u * (gb & 1));
+                    mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
+                    mma_commit_pair_both(s_full(gb & 1));
+                } else {                                     // PV_b
+                    if (!mbar_wait_cluster(p_full, gb & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int m = 0; m < C::PV_ATOMS; ++m, ++pos) {
+                        const int slot = pos % C::NSLOT;
+                        if (!mbar_wait_cluster(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t d = tmem + C::TMEM_O + 128 * (m >> 1);
+                        const uint32_t vb = ring_s + slot * C::ATOM;
+                        const uint32_t po = (uint32_t)(m & 1) * 128 * 64;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {        // 32 keys each
+                            const uint64_t da = desc_sw128_mn(vb + k * 4096, C::ATOM);
+                            mma_f8_pair(d, da, desc_sw64_mn(ph_s + po + k * 2048), idesc_pv,
+                                        (b > 0 || (m & 1) || k > 0) ? 1u : 0u);
+                            mma_f8_pair(d, da, desc_sw64_mn(pl_s + po + k * 2048), idesc_pv, 1u);
+                        }
+                        issued = true;
+                        mma_commit_pair_both(empty(slot));
+                    }
+                    if (!ok) break;
+                    mma_commit_pair_both(pv_done);
+                    if (b == nblocks - 1) mma_commit_pair_both(o_ready);
+                }
+            }
+            gb0 += nblocks;
+            ++nq;
+        }
+        if (!ok) {
+            abort_pair();
+            if (issued) {                                    // nothing may be in flight at dealloc
+                mma_commit_pair_both(drain);
+                mbar_wait(drain, 0);
+            }
+        }
     }
-    if (tid < HG) lse[(int64_t)t * 128 + h0 + tid] = ls[tid] == 0.f ? -INFINITY : ms[tid] + logf(ls[tid]);
+    } else if (warp < C::SOFT0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_PREP));
+        // ------------------------------------------------ units, q, key scales
+        const int pw = warp - C::PREP0;
+        const float sl2 = P.sm_scale * 1.4426950408889634f;
+        const uint32_t q_ready_lead = mapa_shared(q_ready, 0);
+        const uint32_t qsc_peer = mapa_shared(sbase + C::OFF_QS, (uint32_t)peer);
+        if (pw == 0 && lane == 0) prefetch_tmap(&tm_q);
+        bool ok = run;
+        int gb = 0;                                          // blocks so far
+        int nq = 0;                                          // units with blocks so far
+        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
+            const int t = T - 1 - u / nsplit;
+            const int split = u % nsplit;
+            const RowInfo ri = row_info_warp(P, t);
+            const int32_t *irow = idx + (int64_t)t * K;
+            int nblocks;
+            bool okw = true;
+            if (pw == 0) {
+                const Unit un = unit_scan(P, ri, irow, K, split, bps, lane);
+                nblocks = un.nblocks;
+                if (lane == 0) {
+                    if (j >= 2) okw = mbar_wait(unit_free(j & 1), ((j >> 1) - 1) & 1);
+                    if (okw) {
+                        unit_nb[j & 1] = nblocks;
+                        unit_fb[j & 1] = un.fallback;
+                        mbar_arrive(unit_full(j & 1));
+                    }
+                    if (okw && nblocks > 0 && nq > 0) okw = mbar_wait(q_free, (nq - 1) & 1);
+                    if (okw && nblocks > 0) {
+                        mbar_expect_tx(q_raw, C::NQ * C::QATOM);
+                        for (int a = 0; a < C::NQ; ++a)
+                            tma_load_2d(q_s + a * C::QATOM, &tm_q, q_raw, 64 * a, t * 128 + 64 * cr);
+                    }
+                }
+            } else {
+                okw = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+                nblocks = okw ? unit_nb[j & 1] : 0;
+                if (__all_sync(0xffffffffu, okw) && lane == 0) mbar_arrive(unit_free(j & 1));
+            }
+            if (!__all_sync(0xffffffffu, okw) || misc[1]) {
+                // (a q load just issued is waited for below the loop)
+                if (pw == 0 && lane == 0 && okw && nblocks > 0) mbar_wait(q_raw, nq & 1);
+                ok = false;
+                break;
+            }
+            if (nblocks == 0) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait(q_raw, nq & 1))) {
+                ok = false;
+                break;
+            }
+            // ---- split q in place: 8 lanes per head row, each the 16-byte chunk g of the row's nine
+            // 128-byte lines (dims 64 a + 8 g ..); the split row takes the same nine lines
+            const int g8 = lane & 7;
+#pragma unroll 1
+            for (int it = 0; it < 4; ++it) {
+                const int r = 16 * pw + 4 * it + (lane >> 3);
+                unsigned char *line = smem + C::OFF_Q + r * 128;
+                uint4 x[C::NQ];
+#pragma unroll
+                for (int a = 0; a < C::NQ; ++a)
+                    x[a] = *reinterpret_cast<const uint4 *>(line + a * C::QATOM + ((g8 ^ (r & 7)) << 4));
+                auto absmax = [](const uint4 &v, __nv_bfloat162 m) {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+                    return m;
+                };
+                __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+                for (int a = 0; a < 8; ++a) m = absmax(x[a], m);
+                const __nv_bfloat162 mr2 = absmax(x[8], __floats2bfloat162_rn(0.f, 0.f));
+                uint32_t top = max(max(cache::abs_bits(__low2float(m)), cache::abs_bits(__high2float(m))),
+                                   max(cache::abs_bits(__low2float(mr2) * cache::KV8_ROPE_GAIN),
+                                       cache::abs_bits(__high2float(mr2) * cache::KV8_ROPE_GAIN)));
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const uint32_t byte = cache::scale_byte(top);
+                const float inv = cache::scale_inverse(byte);
+                __syncwarp();                                // the rows of this warp are read
+#pragma unroll
+                for (int a = 0; a < C::NQ; ++a) {
+                    const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+                    const float gain = a == 8 ? cache::KV8_ROPE_GAIN : 1.0f;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v0 = __uint_as_float(w[i] << 16), v1 = __uint_as_float(w[i] & 0xffff0000u);
+                        // fp16 holds the 8 significant bits of bf16 down to 2^-24
+                        split_e4m3(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
+                    }
+                    const uint2 h = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                    const uint2 l = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                    // line and 16-byte chunk of the split row: latent dims 128 A .. in atoms A and 4 + A,
+                    // the RoPE dims in atom 8 as [hi | lo]
+                    const int ah = a == 8 ? 8 : a >> 1, al = a == 8 ? 8 : 4 + (a >> 1);
+                    const int ch = (a == 8 ? 0 : (a & 1) * 4) + (g8 >> 1), cl = a == 8 ? 4 + (g8 >> 1) : ch;
+                    *reinterpret_cast<uint2 *>(line + ah * C::QATOM + ((ch ^ (r & 7)) << 4) + 8 * (g8 & 1)) = h;
+                    *reinterpret_cast<uint2 *>(line + al * C::QATOM + ((cl ^ (r & 7)) << 4) + 8 * (g8 & 1)) = l;
+                }
+                if (g8 == 0) {
+                    const int at = 128 * (nq & (C::NQS - 1)) + 64 * cr + r;
+                    const float s = ue8m0_to_float(byte) * sl2;
+                    qsc[at] = s;
+                    st_cluster_u32(qsc_peer + 4u * at, __float_as_uint(s));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(q_ready_lead);
+            ++nq;
+            // ---- scales of this CTA's keys (-1: masked) and the running largest exponent over both
+            // CTAs' keys, block by block
+            const int32_t *irow_s = irow + split * bps * C::BLK;
+            const int ks_left = K - split * bps * C::BLK;
+            const int s_own = 128 * cr + 32 * pw + lane, s_oth = 128 * peer + 32 * pw + lane;
+            auto entry = [&](int s) { return s < ks_left ? __ldg(irow_s + s) : -1; };
+            int e_own = entry(s_own), e_oth = entry(s_oth);
+            int er = C::ER_MIN;
+            for (int b = 0; b < nblocks; ++b, ++gb) {
+                const bool v_own = mla::pair_visible(e_own, ri), v_oth = mla::pair_visible(e_oth, ri);
+                const uint32_t c_own = v_own ? __ldg(kv_scale + key_row(P, ri, e_own)) : 0u;
+                const uint32_t c_oth = v_oth ? __ldg(kv_scale + key_row(P, ri, e_oth)) : 0u;
+                if (b + 1 < nblocks) {
+                    e_own = entry(s_own + C::BLK * (b + 1));
+                    e_oth = entry(s_oth + C::BLK * (b + 1));
+                }
+                // a NaN scale (255) says nothing about the others'
+                const uint32_t top = max(c_own == 255u ? 0u : c_own, c_oth == 255u ? 0u : c_oth);
+                er = max(er, (int)__reduce_max_sync(0xffffffffu, top));
+                const int sl = gb & (C::NINFO - 1);
+                if (gb >= C::NINFO) okw = mbar_wait(info_free(sl), ((gb / C::NINFO) - 1) & 1);
+                if (!__all_sync(0xffffffffu, okw) || misc[1]) {
+                    ok = false;
+                    break;
+                }
+                info[128 * sl + 32 * pw + lane] = v_own ? ue8m0_to_float(c_own) : -1.0f;
+                if (lane == 0) ers[4 * sl + pw] = er;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(info_full(sl));
+            }
+        }
+        if (!ok && lane == 0) abort_pair();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFT));
+        // ------------------------------------------------ softmax + epilogue
+        const int st = tid - 32 * C::SOFT0;                  // 0 .. 255
+        const int quarter = warp & 3;
+        const int h2 = (warp - C::SOFT0) >> 2;               // head half handled by this warp
+        const int key = quarter * 32 + lane;                 // this thread's key among the CTA's 128
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t xm_peer = mapa_shared(sbase + C::OFF_XM, (uint32_t)peer);
+        const uint32_t xbar_peer = mapa_shared(xbar(0), (uint32_t)peer);
+        const uint32_t s_free_lead = mapa_shared(s_free(0), 0);
+        const uint32_t p_full_lead = mapa_shared(p_full, 0);
+        // row 128 cr + key of the P'^T buffers of the CTA holding heads 64 h2 .. + 63
+        const uint32_t prow = (uint32_t)(128 * cr + key);
+        const uint32_t ph_row = (h2 == cr ? ph_s : mapa_shared(ph_s, (uint32_t)peer)) + prow * 64;
+        const uint32_t pl_row = ph_row + (C::OFF_PL - C::OFF_PH);
+        const uint32_t pswz = (prow >> 1) & 3;
+        bool ok = run;
+        int gb0 = 0;                                         // blocks of the earlier units
+        int nq = 0;                                          // units with blocks so far
+        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
+            const int t = T - 1 - u / nsplit;
+            const int split = u % nsplit;
+            const bool got = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+            const int nblocks = got ? unit_nb[j & 1] : 0;
+            if (named_bar_or(1, 256, !got || misc[1] != 0)) {
+                ok = false;
+                break;
+            }
+            if (st == 0) mbar_arrive(unit_free(j & 1));
+            if (st < 128) mr[st] = -INFINITY;                // reference maxima of the 128 heads
+            const float *qs = qsc + 128 * (nq & (C::NQS - 1));
+            float l[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) l[i] = 0.f;
+            int er = C::ER_MIN;
+            for (int b = 0; b < nblocks; ++b) {
+                const int gb = gb0 + b;
+                const int sl = gb & (C::NINFO - 1);
+                const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
+                                  !mbar_wait_cluster(s_full(gb & 1), (gb >> 1) & 1);
+                if (named_bar_or(1, 256, fail)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float ks = info[128 * sl + key];
+                const int4 er4 = reinterpret_cast<const int4 *>(ers)[sl];
+                const int er_new = max(max(er4.x, er4.y), max(er4.z, er4.w));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(info_free(sl));
+                const bool vis = !(ks < 0.f);
+                const uint32_t sb = t_lane + C::TMEM_S + 128 * (gb & 1) + 64 * h2;
+                // ---- block maxima of this CTA's keys (per head), then of the pair
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    uint32_t sr[32];
+                    tmem_ld32(sb + 32 * jj, sr);
+                    tmem_wait_ld();
+                    float mine = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float r = warp_fmax(vis ? __uint_as_float(sr[i]) * ks : -INFINITY);
+                        mine = lane == i ? r : mine;
+                    }
+                    red[quarter * 128 + 64 * h2 + 32 * jj + lane] = mine;
+                }
+                named_bar(1, 256);
+                bool need = false;
+                if (st < 128) {
+                    const int h = st;
+                    const float m_cta = fmaxf(fmaxf(red[h], red[128 + h]), fmaxf(red[256 + h], red[384 + h]));
+                    st_async_f32(xm_peer + 4u * (128 * (gb & 1) + h), m_cta, xbar_peer + 8u * (gb & 1));
+                    if (st == 0) mbar_expect_tx(xbar(gb & 1), 128 * 4);
+                    const bool okx = mbar_wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
+                    const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * qs[h];
+                    const float m_old = mr[h];
+                    need = m_blk > m_old + C::TAU;
+                    const float m_new = need ? m_blk : m_old;
+                    fs[h] = (need && m_old != -INFINITY) ? exp2f(m_old - m_new) : 1.0f;
+                    mr[h] = m_new;
+                    if (!okx) misc[1] = 1;
+                }
+                // every exit decision below is taken through a barrier, so the 8 warps stay together
+                const bool any = named_bar_or(1, 256, need);
+                // PV_{b-1} has read P'^T and, for a rescale, O^T is whole (block 0's predecessor, the
+                // previous unit's last PV, completed before that unit's epilogue)
+                bool okp = true;
+                if (b > 0) okp = mbar_wait_cluster(pv_done, (gb - 1) & 1);
+                if (!okp) misc[1] = 1;
+                if (any) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) l[i] *= fs[64 * h2 + i];
+                }
+                if (b > 0 && (any || er_new != er) && __all_sync(0xffffffffu, okp)) {
+                    tc_fence_after();
+                    const float fe = exp2f((float)(er - er_new));
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t o[32];
+                        const uint32_t oa = t_lane + C::TMEM_O + 128 * h2 + 32 * ch;
+                        tmem_ld32(oa, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * (fs[32 * ch + i] * fe));
+                        tmem_st32(oa, o);
+                    }
+                    tmem_wait_st();
+                }
+                er = er_new;
+                // ---- P'^T of this thread's key for its 64 heads
+                const float kf = vis ? ks * __uint_as_float((uint32_t)min(254 + C::BASE - er, 254) << 23) : 0.f;
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    uint32_t sr[32], hi[8], lo[8];
+                    tmem_ld32(sb + 32 * jj, sr);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int h = 32 * jj + 2 * i;
+                        const float2 m2 = reinterpret_cast<const float2 *>(mr)[32 * h2 + 16 * jj + i];
+                        const float2 q2 = reinterpret_cast<const float2 *>(qs)[32 * h2 + 16 * jj + i];
+                        const float p0 = vis ? ex2_approx(fmaf(__uint_as_float(sr[2 * i]) * ks, q2.x, -m2.x)) : 0.f;
+                        const float p1 = vis ? ex2_approx(fmaf(__uint_as_float(sr[2 * i + 1]) * ks, q2.y, -m2.y)) : 0.f;
+                        l[h] += p0;
+                        l[h + 1] += p1;
+                        uint32_t hh, ll;
+                        split_e4m3(__floats2half2_rn(p0 * kf, p1 * kf), hh, ll);
+                        hi[i >> 1] = (i & 1) ? hi[i >> 1] | hh << 16 : hh;
+                        lo[i >> 1] = (i & 1) ? lo[i >> 1] | ll << 16 : ll;
+                    }
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const uint32_t off = ((2 * jj + v) ^ pswz) << 4;
+                        if (h2 == cr) {
+                            st_shared_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
+                            st_shared_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+                        } else {
+                            st_cluster_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
+                            st_cluster_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                if (h2 == cr) fence_proxy_async_smem();
+                else fence_proxy_async_cluster();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(s_free_lead + 8u * (gb & 1));   // S^T consumed
+                    mbar_arrive_cluster(p_full_lead);                   // this warp's 32 rows are in place
+                }
+                if (named_bar_or(1, 256, misc[1] != 0)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok && st == 0) abort_pair();
+
+            // ---- epilogue: row sums of the pair, lse, O^T / l transposed into out
+            const int64_t obase = (int64_t)t * 128;
+            const int64_t pbase = ((int64_t)t * nsplit + split) * 128;   // partial rows (split mode)
+            if (nblocks > 0 && ok) {
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = l[32 * jj + i];
+                    red[quarter * 128 + 64 * h2 + 32 * jj + lane] = mla::transpose_reduce32<false>(v, lane);
+                }
+                named_bar(1, 256);
+                if (st < 128) {
+                    const int h = st;
+                    const float l_cta = (red[h] + red[128 + h]) + (red[256 + h] + red[384 + h]);
+                    st_async_f32(mapa_shared(sbase + C::OFF_XL + 4u * h, (uint32_t)peer), l_cta,
+                                 mapa_shared(lbar, (uint32_t)peer));
+                    if (st == 0) mbar_expect_tx(lbar, 128 * 4);
+                    const bool okl = mbar_wait_cluster(lbar, nq & 1);
+                    // the two CTAs add the same two numbers in the same order
+                    const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
+                    // O^T holds sum p 2^(e - er + BASE) code
+                    fs[h] = okl && l_tot != 0.f ? ue8m0_to_float((uint32_t)(er - C::BASE)) / l_tot : 0.f;
+                    if ((h >> 6) == cr) {
+                        const float lv =
+                            okl ? (l_tot != 0.f ? (mr[h] + log2f(l_tot)) * 0.6931471805599453f : -INFINITY) : NAN;
+                        if (SPLIT) sp.lse_part[pbase + h] = lv;
+                        else lse[obase + h] = lv;
+                    }
+                }
+                const bool oko = mbar_wait_cluster(o_ready, nq & 1);
+                named_bar(1, 256);
+                tc_fence_after();
+                // O^T block i = h2: lanes = value dims 256 h2 + 128 cr + quarter*32 + lane, columns = heads
+                if (SPLIT) {   // fp32 partial rows, written from registers (32 lanes: 128 bytes per head)
+                    float *op = sp.o_part + pbase * 512 + 256 * h2 + 128 * cr + key;
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t o[32];
+                        tmem_ld32(t_lane + C::TMEM_O + 128 * h2 + 32 * ch, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int h = 32 * ch + i;
+                            op[(int64_t)h * 512] = oko ? __uint_as_float(o[i]) * fs[h] : NAN;
+                        }
+                    }
+                } else {
+                    // bf16 rows from registers: lanes 2m and 2m + 1 swap one value per head pair, so
+                    // each stores two adjacent dims of one head (64 contiguous bytes per head per warp)
+                    const bool odd = (lane & 1) != 0;
+                    __nv_bfloat16 *orow = out + obase * 512 + 256 * h2 + 128 * cr + 32 * quarter + (lane & ~1);
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t o[32];
+                        tmem_ld32(t_lane + C::TMEM_O + 128 * h2 + 32 * ch, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const int h = 32 * ch + i;
+                            const float v0 = oko ? __uint_as_float(o[i]) * fs[h] : NAN;
+                            const float v1 = oko ? __uint_as_float(o[i + 1]) * fs[h + 1] : NAN;
+                            const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                            const uint32_t w = odd ? pack_bf16x2(recv, v1) : pack_bf16x2(v0, recv);
+                            *reinterpret_cast<uint32_t *>(orow + (int64_t)(h + (odd ? 1 : 0)) * 512) = w;
+                        }
+                    }
+                }
+                // O^T read out: ordered before this warp's next arrivals (s_free, p_full) by the
+                // tcgen05 fence that precedes them
+            } else {
+                // no visible slot: out = 0, lse = -inf (an aborted pipeline: NaN)
+                const uint32_t fill = nblocks == 0 ? 0u : 0x7fc07fc0u;
+                for (int e = st; e < 128 * 32; e += 256) {
+                    const int h = e >> 5, part = e & 31;      // 32 x 16 bytes per head: the CTA's 2 x 128 dims
+                    const int d0 = 256 * (part >> 4) + 128 * cr + 8 * (part & 15);
+                    if (SPLIT) {
+                        const float f = __uint_as_float(nblocks == 0 ? 0u : 0x7fc00000u);
+                        float4 *op = reinterpret_cast<float4 *>(sp.o_part + (pbase + h) * 512 + d0);
+                        op[0] = make_float4(f, f, f, f);
+                        op[1] = make_float4(f, f, f, f);
+                    } else {
+                        *reinterpret_cast<uint4 *>(out + (obase + h) * 512 + d0) = make_uint4(fill, fill, fill, fill);
+                    }
+                }
+                if (st < 128 && (st >> 6) == cr) {
+                    const float lv = nblocks == 0 ? -INFINITY : NAN;
+                    if (SPLIT) sp.lse_part[pbase + st] = lv;
+                    else lse[obase + st] = lv;
+                }
+            }
+            gb0 += nblocks;
+            if (nblocks > 0) ++nq;
+        }
+    }
+    // ---- teardown: nothing of either CTA is in flight past this point.  After an abort
+    // (either CTA's flag, so both take the same branch) the even CTA first waits, bounded,
+    // until the last position either CTA issued into each slot has landed.  Each CTA hands
+    // its final flag to the peer before the cluster barrier: past that barrier the peer may
+    // already have exited, so nothing reads the peer's shared memory there.
+    tc_fence_before();
+    __syncthreads();                                         // this CTA's roles are done
+    if (tid == 0) st_cluster_u32(mapa_shared(sbase + C::OFF_MISC + 24, (uint32_t)peer), misc[1]);
+    cluster_sync();
+    const bool aborted = misc[1] != 0u || misc[6] != 0u;     // the same in both CTAs
+    if (aborted) {
+        if (cr == 0 && run && tid < C::NSLOT) {
+            const int *lp = reinterpret_cast<const int *>(smem + C::OFF_LASTPOS);
+            const int pmax = max(lp[tid], lp[C::NSLOT + tid]);
+            if (pmax >= 0) mbar_wait_cluster(pfull(tid), (uint32_t)(pmax / C::NSLOT) & 1u);
+        }
+        cluster_sync();
+    }
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
 }
 
 }  // namespace mla8
