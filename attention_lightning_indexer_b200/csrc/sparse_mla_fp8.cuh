@@ -17,6 +17,12 @@
 // RoPE dims are taken 16 times: the K axis is 4 atoms of latent codes and one atom [hi | lo],
 // multiplied by the same 64 RoPE dims of q twice.
 //
+// Hand-overs between the CTAs avoid cluster-scope fences, which cost 1.5 to 2 us each beside
+// the DSMEM traffic: the half of P'^T that belongs to the other CTA's heads goes there by
+// st.async, which counts its bytes on that CTA's barrier p_in (the odd CTA's warp 7 relays it
+// to the MMA thread), and the other arrivals carry nothing but the order of the tcgen05 and
+// proxy fences before them.
+//
 // The schedule is that of the bf16 kernel (sparse_mla_pair.cuh): persistent CTA pairs take
 // (token, split) units in turn; blocks of 256 index slots, CTA c owns slots 128 c .. + 127 of
 // each block and heads 64 c .. + 63;
@@ -72,8 +78,8 @@ struct Cfg {
     static constexpr int OFF_ER = OFF_INFO + NINFO * 128 * 4;   // [NINFO][4] int, running maxima of exponents
     static constexpr int OFF_BAR = OFF_ER + NINFO * 4 * 4;
     // empty[7] pfull[7] q_raw q_ready q_free s_full[2] s_free[2] p_full pv_done o_ready xbar[2] lbar
-    // drain unit_full[2] unit_free[2] info_full[4] info_free[4]
-    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO;
+    // drain unit_full[2] unit_free[2] info_full[4] info_free[4] p_in
+    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO + 1;
     // [0] TMEM base, [1] abort, [2..3] unit blocks, [4..5] unit fallback keys, [6] peer's abort flag
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
     static constexpr int OFF_LASTPOS = OFF_MISC + 32;           // even CTA: [2][NSLOT] last ring position issued
@@ -202,7 +208,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const uint32_t q_free = q_raw + 16;                      // the unit's last QK has read q_s
     auto s_full = [&](int b) { return q_raw + 24 + 8u * b; };
     auto s_free = [&](int b) { return q_raw + 40 + 8u * b; };
-    const uint32_t p_full = q_raw + 56;                      // P'^T of both CTAs written (even CTA)
+    const uint32_t p_full = q_raw + 56;                      // even CTA: P'^T in place, but for p_in
     const uint32_t pv_done = q_raw + 64;
     const uint32_t o_ready = q_raw + 72;
     auto xbar = [&](int b) { return q_raw + 80 + 8u * b; };
@@ -212,6 +218,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     auto unit_free = [&](int i) { return q_raw + 128 + 8u * i; };
     auto info_full = [&](int i) { return q_raw + 144 + 8u * i; };
     auto info_free = [&](int i) { return q_raw + 144 + 8u * (C::NINFO + i); };
+    const uint32_t p_in = q_raw + 144 + 8u * (2 * C::NINFO); // P'^T rows of the peer's keys landed here
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
     volatile int *unit_nb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
     volatile int *unit_fb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);
@@ -230,9 +237,10 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             mbar_init(s_free(b), 16);     // 8 softmax warps of each CTA
             mbar_init(xbar(b), 1);
             mbar_init(unit_full(b), 1);   // warp 8
-            mbar_init(unit_free(b), C::NLOAD + 3 + 1 + (cr == 0 ? 1 : 0));
+            mbar_init(unit_free(b), C::NLOAD + 3 + 1 + 1);   // gathers, preparing warps, softmax, MMA or relay
         }
-        mbar_init(p_full, 16);            // 8 softmax warps of each CTA
+        mbar_init(p_full, 9);             // 4 warps of each CTA (own rows), the odd CTA's relay
+        mbar_init(p_in, 1);
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(lbar, 1);
@@ -350,7 +358,24 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (lane == 0)
             st_cluster_u32(mapa_shared(sbase + C::OFF_LASTPOS + 4u * (uint32_t)(cr * C::NSLOT + lw), 0),
                            (uint32_t)last_issued);
-    } else if (lane == 0 && cr == 0) {
+    } else if (lane == 0 && cr == 1) {
+        // ------------------------------------------------ relay (odd CTA): the peer's rows of P'^T
+        const uint32_t p_full_lead = mapa_shared(p_full, 0);
+        bool ok = run;
+        int gb = 0;
+        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
+            ok = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+            const int nblocks = ok ? unit_nb[j & 1] : 0;
+            if (ok) mbar_arrive(unit_free(j & 1));
+            for (int b = 0; ok && b < nblocks; ++b, ++gb) {
+                mbar_expect_tx(p_in, 128 * 128);
+                ok = mbar_wait_cluster(p_in, gb & 1) && !misc[1];
+                fence_proxy_async_smem();
+                if (ok) mbar_arrive_remote(p_full_lead);
+            }
+        }
+        if (!ok) abort_pair();
+    } else if (lane == 0) {
         // ------------------------------------------------ MMA issuer (even CTA)
         const uint32_t idesc_qk = idesc_e4m3(256, 128);
         const uint32_t idesc_pv = idesc_e4m3(256, 128) | (1u << 15) | (1u << 16);   // A and B MN-major
@@ -378,7 +403,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 mla::pair_group(g, nblocks, qk, b);
                 const int gb = gb0 + b;
                 if (qk) {                                    // QK_b -> S^T buffer gb & 1
-                    if (gb >= 2 && !mbar_wait_cluster(s_free(gb & 1), ((gb >> 1) - 1) & 1)) {
+                    if (gb >= 2 && !mbar_wait(s_free(gb & 1), ((gb >> 1) - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -386,7 +411,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const uint32_t d = tmem + C::TMEM_S + 128 * (gb & 1);
                     for (int a = 0; a < C::QK_ATOMS; ++a, ++pos) {
                         const int slot = pos % C::NSLOT;
-                        if (!mbar_wait_cluster(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
+                        if (!mbar_wait(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
                             ok = false;
                             break;
                         }
@@ -408,20 +433,27 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                     if (!ok) break;
                     if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
-                    // this thread's own arrivals pass on what it has seen (the q scales, through
-                    // q_ready) to the softmax warps that wait for S^T
-                    mbar_arrive_cluster(s_full_own + 8u * (gb & 1));
-                    mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
+                    // this thread's own arrivals for a unit's first block pass on what it has seen (the
+                    // q scales, through q_ready) to the softmax warps that wait for S^T
+                    if (b == 0) {
+                        mbar_arrive_cluster(s_full_own + 8u * (gb & 1));
+                        mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
+                    } else {
+                        mbar_arrive(s_full(gb & 1));
+                        mbar_arrive_remote(s_full_peer + 8u * (gb & 1));
+                    }
                     mma_commit_pair_both(s_full(gb & 1));
                 } else {                                     // PV_b
-                    if (!mbar_wait_cluster(p_full, gb & 1)) {
+                    mbar_expect_tx(p_in, 128 * 128);
+                    if (!mbar_wait(p_full, gb & 1) || !mbar_wait_cluster(p_in, gb & 1)) {
                         ok = false;
                         break;
                     }
+                    fence_proxy_async_smem();
                     tc_fence_after();
                     for (int m = 0; m < C::PV_ATOMS; ++m, ++pos) {
                         const int slot = pos % C::NSLOT;
-                        if (!mbar_wait_cluster(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
+                        if (!mbar_wait(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
                             ok = false;
                             break;
                         }
@@ -610,6 +642,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint32_t xbar_peer = mapa_shared(xbar(0), (uint32_t)peer);
         const uint32_t s_free_lead = mapa_shared(s_free(0), 0);
         const uint32_t p_full_lead = mapa_shared(p_full, 0);
+        const uint32_t p_in_peer = mapa_shared(p_in, (uint32_t)peer);
         // row 128 cr + key of the P'^T buffers of the CTA holding heads 64 h2 .. + 63
         const uint32_t prow = (uint32_t)(128 * cr + key);
         const uint32_t ph_row = (h2 == cr ? ph_s : mapa_shared(ph_s, (uint32_t)peer)) + prow * 64;
@@ -638,7 +671,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const int gb = gb0 + b;
                 const int sl = gb & (C::NINFO - 1);
                 const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
-                                  !mbar_wait_cluster(s_full(gb & 1), (gb >> 1) & 1);
+                                  !(b == 0 ? mbar_wait_cluster(s_full(gb & 1), (gb >> 1) & 1)
+                                           : mbar_wait(s_full(gb & 1), (gb >> 1) & 1));
                 if (named_bar_or(1, 256, fail)) {
                     ok = false;
                     break;
@@ -686,7 +720,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 // PV_{b-1} has read P'^T and, for a rescale, O^T is whole (block 0's predecessor, the
                 // previous unit's last PV, completed before that unit's epilogue)
                 bool okp = true;
-                if (b > 0) okp = mbar_wait_cluster(pv_done, (gb - 1) & 1);
+                if (b > 0) okp = mbar_wait(pv_done, (gb - 1) & 1);
                 if (!okp) misc[1] = 1;
                 if (any) {
 #pragma unroll
@@ -697,6 +731,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float fe = exp2f((float)(er - er_new));
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
+                        // heads whose reference stayed need no pass over their columns
+                        if (er_new == er && __all_sync(0xffffffffu, fs[32 * ch + lane] == 1.0f)) continue;
                         uint32_t o[32];
                         const uint32_t oa = t_lane + C::TMEM_O + 128 * h2 + 32 * ch;
                         tmem_ld32(oa, o);
@@ -737,18 +773,17 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             st_shared_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
                             st_shared_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
                         } else {
-                            st_cluster_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
-                            st_cluster_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+                            st_async_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3], p_in_peer);
+                            st_async_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3], p_in_peer);
                         }
                     }
                 }
                 tc_fence_before();
                 if (h2 == cr) fence_proxy_async_smem();
-                else fence_proxy_async_cluster();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive_cluster(s_free_lead + 8u * (gb & 1));   // S^T consumed
-                    mbar_arrive_cluster(p_full_lead);                   // this warp's 32 rows are in place
+                    mbar_arrive_remote(s_free_lead + 8u * (gb & 1));    // S^T consumed
+                    if (h2 == cr) mbar_arrive_remote(p_full_lead);      // this warp's 32 rows are in place
                 }
                 if (named_bar_or(1, 256, misc[1] != 0)) {
                     ok = false;
@@ -787,7 +822,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         else lse[obase + h] = lv;
                     }
                 }
-                const bool oko = mbar_wait_cluster(o_ready, nq & 1);
+                const bool oko = mbar_wait(o_ready, nq & 1);
                 named_bar(1, 256);
                 tc_fence_after();
                 // O^T block i = h2: lanes = value dims 256 h2 + 128 cr + quarter*32 + lane, columns = heads
