@@ -71,8 +71,8 @@ struct Cfg {
     static constexpr int OFF_RED = OFF_RING + NSLOT * ATOM;     // [4][128] f32
     static constexpr int OFF_XM = OFF_RED + 4 * 128 * 4;        // [2][128] f32, peer block maxima
     static constexpr int OFF_XL = OFF_XM + 2 * 128 * 4;         // [128] f32, peer row sums
-    static constexpr int OFF_MR = OFF_XL + 128 * 4;             // [128] f32, reference maxima
-    static constexpr int OFF_FS = OFF_MR + 128 * 4;             // [128] f32, rescale factor / output factor
+    static constexpr int OFF_MQ = OFF_XL + 128 * 4;             // [64] {-m, -m', qs, qs'} of a head pair
+    static constexpr int OFF_FS = OFF_MQ + 64 * 16;             // [128] f32, rescale factor / output factor
     static constexpr int OFF_QS = OFF_FS + 128 * 4;             // [NQS][128] f32, 2^f[h] * sm_scale * log2 e
     static constexpr int OFF_INFO = OFF_QS + NQS * 128 * 4;     // [NINFO][128] f32, key scale or -1 (masked)
     static constexpr int OFF_ER = OFF_INFO + NINFO * 128 * 4;   // [NINFO][4] int, running maxima of exponents
@@ -195,7 +195,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
     float *xm = reinterpret_cast<float *>(smem + C::OFF_XM);
     float *xl = reinterpret_cast<float *>(smem + C::OFF_XL);
-    float *mr = reinterpret_cast<float *>(smem + C::OFF_MR);
+    float *mq = reinterpret_cast<float *>(smem + C::OFF_MQ);
     float *fs = reinterpret_cast<float *>(smem + C::OFF_FS);
     float *qsc = reinterpret_cast<float *>(smem + C::OFF_QS);
     float *info = reinterpret_cast<float *>(smem + C::OFF_INFO);
@@ -263,8 +263,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
-    const bool run = !misaligned;
+    const uint32_t tmem = misc[0];   // 0: all 512 columns (the MMA warp counts on it)
+    const bool run = !misaligned && tmem == 0;
+    if (tid == 0 && tmem != 0) raise_error(ERR_SMEM_ALIGN);
     const uint32_t peer_misc1 = mapa_shared(sbase + C::OFF_MISC + 4, (uint32_t)peer);
     auto abort_pair = [&]() {                                // stop both CTAs of the pair
         misc[1] = 1;
@@ -375,25 +376,30 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
         }
         if (!ok) abort_pair();
-    } else if (lane == 0) {
+    } else if (cr == 0) {
         // ------------------------------------------------ MMA issuer (even CTA)
+        // The whole warp runs the loop and one elected lane issues, so that descriptors stay in
+        // uniform registers; a lane of its own spent as long on issuing an MMA as it takes to run.
         const uint32_t idesc_qk = idesc_e4m3(256, 128);
         const uint32_t idesc_pv = idesc_e4m3(256, 128) | (1u << 15) | (1u << 16);   // A and B MN-major
-        const uint32_t s_full_own = mapa_shared(s_full(0), 0), s_full_peer = mapa_shared(s_full(0), 1);
+        // descriptors step by bytes / 16 in their low word
+        const uint64_t dq = desc_sw128(q_s), da_k = desc_sw128(ring_s), da_mn = desc_sw128_mn(ring_s, C::ATOM);
+        const uint64_t dph = desc_sw64_mn(ph_s);
+        const uint32_t s_full_peer = mapa_shared(s_full(0), 1);
         bool ok = run;
         bool issued = false;
-        int pos = 0;                                         // ring position, counted across units
+        int slot = 0, phase = 0;                             // ring slot and its phase
         int gb0 = 0;                                         // blocks of the earlier units
         int nq = 0;                                          // units with blocks so far
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
-            if (!mbar_wait(unit_full(j & 1), (j >> 1) & 1)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(unit_full(j & 1), (j >> 1) & 1))) {
                 ok = false;
                 break;
             }
-            const int nblocks = unit_nb[j & 1];
-            mbar_arrive(unit_free(j & 1));
+            const int nblocks = __shfl_sync(0xffffffffu, unit_nb[j & 1], 0);
+            if (elect_one()) mbar_arrive(unit_free(j & 1));
             if (nblocks == 0) continue;
-            if (!mbar_wait_cluster(q_ready, nq & 1) || misc[1]) {
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(q_ready, nq & 1))) {
                 ok = false;
                 break;
             }
@@ -403,85 +409,98 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 mla::pair_group(g, nblocks, qk, b);
                 const int gb = gb0 + b;
                 if (qk) {                                    // QK_b -> S^T buffer gb & 1
-                    if (gb >= 2 && !mbar_wait(s_free(gb & 1), ((gb >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    bool okw = gb < 2 || mbar_wait(s_free(gb & 1), ((gb >> 1) - 1) & 1);
                     tc_fence_after();
-                    const uint32_t d = tmem + C::TMEM_S + 128 * (gb & 1);
-                    for (int a = 0; a < C::QK_ATOMS; ++a, ++pos) {
-                        const int slot = pos % C::NSLOT;
-                        if (!mbar_wait(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t sa = ring_s + slot * C::ATOM;
+                    const uint32_t d = C::TMEM_S + 128 * (gb & 1);
+#pragma unroll
+                    for (int a = 0; a < C::QK_ATOMS; ++a) {
+                        okw = okw && mbar_wait(pfull(slot), phase);
                         // q: hi and lo atoms of the same 128 dims; for the RoPE atom [hi | lo] of the
                         // keys, 64 dims of q hi and lo twice
-                        const bool rope = a == C::QK_ATOMS - 1;
-                        const uint32_t qh = q_s + (rope ? 8 : a) * C::QATOM;
-                        const uint32_t ql = rope ? qh + 64 : q_s + (4 + a) * C::QATOM;
+                        constexpr int ROPE = C::QK_ATOMS - 1;
+                        const uint64_t da = da_k + (uint64_t)(slot * (C::ATOM >> 4));
+                        const uint64_t qh = dq + (uint64_t)((a == ROPE ? 8 : a) * (C::QATOM >> 4));
+                        const uint64_t ql = a == ROPE ? qh + 4 : dq + (uint64_t)((4 + a) * (C::QATOM >> 4));
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint32_t qo = 32u * (rope ? (kk & 1) : kk);
-                            const uint64_t da = desc_sw128(sa + kk * 32);
-                            mma_f8_pair(d, da, desc_sw128(qh + qo), idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
-                            mma_f8_pair(d, da, desc_sw128(ql + qo), idesc_qk, 1u);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const int qo = 2 * (a == ROPE ? (kk & 1) : kk);
+                                mma_f8_pair(d, da + 2 * kk, qh + qo, idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
+                                mma_f8_pair(d, da + 2 * kk, ql + qo, idesc_qk, 1u);
+                            }
+                            mma_commit_pair_both(empty(slot));
                         }
-                        issued = true;
-                        mma_commit_pair_both(empty(slot));
+                        if (++slot == C::NSLOT) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
-                    if (!ok) break;
-                    if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
-                    // this thread's own arrivals for a unit's first block pass on what it has seen (the
-                    // q scales, through q_ready) to the softmax warps that wait for S^T
-                    if (b == 0) {
-                        mbar_arrive_cluster(s_full_own + 8u * (gb & 1));
-                        mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
-                    } else {
-                        mbar_arrive(s_full(gb & 1));
-                        mbar_arrive_remote(s_full_peer + 8u * (gb & 1));
+                    if (elect_one()) {
+                        if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
+                        // this thread's own arrivals for a unit's first block pass on what it has seen
+                        // (the q scales, through q_ready) to the softmax warps that wait for S^T
+                        if (b == 0) {
+                            mbar_arrive_cluster(s_full(gb & 1));
+                            mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
+                        } else {
+                            mbar_arrive(s_full(gb & 1));
+                            mbar_arrive_remote(s_full_peer + 8u * (gb & 1));
+                        }
+                        mma_commit_pair_both(s_full(gb & 1));
                     }
-                    mma_commit_pair_both(s_full(gb & 1));
+                    issued = true;
+                    if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
                 } else {                                     // PV_b
-                    mbar_expect_tx(p_in, 128 * 128);
-                    if (!mbar_wait(p_full, gb & 1) || !mbar_wait_cluster(p_in, gb & 1)) {
-                        ok = false;
-                        break;
+                    // the four atoms first: they landed long before P'^T as a rule
+                    bool okw = true;
+                    int sl = slot, ph = phase;
+#pragma unroll
+                    for (int m = 0; m < C::PV_ATOMS; ++m) {
+                        okw = okw && mbar_wait(pfull(sl), ph);
+                        if (++sl == C::NSLOT) {
+                            sl = 0;
+                            ph ^= 1;
+                        }
                     }
+                    if (elect_one()) mbar_expect_tx(p_in, 128 * 128);
+                    okw = okw && mbar_wait(p_full, gb & 1) && mbar_wait_cluster(p_in, gb & 1);
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    for (int m = 0; m < C::PV_ATOMS; ++m, ++pos) {
-                        const int slot = pos % C::NSLOT;
-                        if (!mbar_wait(pfull(slot), (pos / C::NSLOT) & 1) || misc[1]) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t d = tmem + C::TMEM_O + 128 * (m >> 1);
-                        const uint32_t vb = ring_s + slot * C::ATOM;
-                        const uint32_t po = (uint32_t)(m & 1) * 128 * 64;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {        // 32 keys each
-                            const uint64_t da = desc_sw128_mn(vb + k * 4096, C::ATOM);
-                            mma_f8_pair(d, da, desc_sw64_mn(ph_s + po + k * 2048), idesc_pv,
-                                        (b > 0 || (m & 1) || k > 0) ? 1u : 0u);
-                            mma_f8_pair(d, da, desc_sw64_mn(pl_s + po + k * 2048), idesc_pv, 1u);
+                    for (int m = 0; m < C::PV_ATOMS; ++m) {
+                        const uint32_t d = C::TMEM_O + 128 * (m >> 1);
+                        const uint64_t da = da_mn + (uint64_t)(slot * (C::ATOM >> 4));
+                        const uint64_t db = dph + (uint64_t)((m & 1) * (128 * 64 >> 4));
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {    // 32 keys each
+                                mma_f8_pair(d, da + k * (4096 >> 4), db + k * (2048 >> 4), idesc_pv,
+                                            (b > 0 || (m & 1) || k > 0) ? 1u : 0u);
+                                mma_f8_pair(d, da + k * (4096 >> 4), db + ((C::OFF_PL - C::OFF_PH) >> 4) + k * (2048 >> 4),
+                                            idesc_pv, 1u);
+                            }
+                            mma_commit_pair_both(empty(slot));
                         }
-                        issued = true;
-                        mma_commit_pair_both(empty(slot));
+                        if (++slot == C::NSLOT) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
-                    if (!ok) break;
-                    mma_commit_pair_both(pv_done);
-                    if (b == nblocks - 1) mma_commit_pair_both(o_ready);
+                    if (elect_one()) {
+                        mma_commit_pair_both(pv_done);
+                        if (b == nblocks - 1) mma_commit_pair_both(o_ready);
+                    }
+                    issued = true;
+                    if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
                 }
             }
             gb0 += nblocks;
             ++nq;
         }
         if (!ok) {
-            abort_pair();
+            if (lane == 0) abort_pair();
             if (issued) {                                    // nothing may be in flight at dealloc
-                mma_commit_pair_both(drain);
+                if (elect_one()) mma_commit_pair_both(drain);
                 mbar_wait(drain, 0);
             }
         }
@@ -661,11 +680,12 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 break;
             }
             if (st == 0) mbar_arrive(unit_free(j & 1));
-            if (st < 128) mr[st] = -INFINITY;                // reference maxima of the 128 heads
+            const int mqh = (st >> 1) * 4 + (st & 1);        // st < 128: this thread's head in mq
+            if (st < 128) mq[mqh] = INFINITY;                // minus the reference maximum
             const float *qs = qsc + 128 * (nq & (C::NQS - 1));
-            float l[64];
+            uint64_t l[32];                                  // row sums of head pairs
 #pragma unroll
-            for (int i = 0; i < 64; ++i) l[i] = 0.f;
+            for (int i = 0; i < 32; ++i) l[i] = 0ull;
             int er = C::ER_MIN;
             for (int b = 0; b < nblocks; ++b) {
                 const int gb = gb0 + b;
@@ -673,10 +693,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
                                   !(b == 0 ? mbar_wait_cluster(s_full(gb & 1), (gb >> 1) & 1)
                                            : mbar_wait(s_full(gb & 1), (gb >> 1) & 1));
-                if (named_bar_or(1, 256, fail)) {
-                    ok = false;
-                    break;
-                }
+                __syncwarp();
                 tc_fence_after();
                 const float ks = info[128 * sl + key];
                 const int4 er4 = reinterpret_cast<const int4 *>(ers)[sl];
@@ -699,42 +716,58 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                     red[quarter * 128 + 64 * h2 + 32 * jj + lane] = mine;
                 }
-                named_bar(1, 256);
+                // every exit decision is taken through a barrier, so the 8 warps stay together
+                if (named_bar_or(1, 256, fail)) {
+                    ok = false;
+                    break;
+                }
                 bool need = false;
                 if (st < 128) {
                     const int h = st;
                     const float m_cta = fmaxf(fmaxf(red[h], red[128 + h]), fmaxf(red[256 + h], red[384 + h]));
                     st_async_f32(xm_peer + 4u * (128 * (gb & 1) + h), m_cta, xbar_peer + 8u * (gb & 1));
                     if (st == 0) mbar_expect_tx(xbar(gb & 1), 128 * 4);
+                    const float q = qs[h];
+                    if (b == 0) mq[mqh + 2] = q;
+                    const float m_old = -mq[mqh];
                     const bool okx = mbar_wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
-                    const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * qs[h];
-                    const float m_old = mr[h];
+                    const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * q;
                     need = m_blk > m_old + C::TAU;
-                    const float m_new = need ? m_blk : m_old;
-                    fs[h] = (need && m_old != -INFINITY) ? exp2f(m_old - m_new) : 1.0f;
-                    mr[h] = m_new;
+                    fs[h] = (need && m_old != -INFINITY) ? exp2f(m_old - m_blk) : 1.0f;
+                    if (need) mq[mqh] = -m_blk;
                     if (!okx) misc[1] = 1;
                 }
-                // every exit decision below is taken through a barrier, so the 8 warps stay together
                 const bool any = named_bar_or(1, 256, need);
                 // PV_{b-1} has read P'^T and, for a rescale, O^T is whole (block 0's predecessor, the
                 // previous unit's last PV, completed before that unit's epilogue)
                 bool okp = true;
                 if (b > 0) okp = mbar_wait(pv_done, (gb - 1) & 1);
                 if (!okp) misc[1] = 1;
-                if (any) {
+                __syncwarp();
+                if (b > 0 && any) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) l[i] *= fs[64 * h2 + i];
+                    for (int i = 0; i < 32; ++i)
+                        l[i] = mul_f32x2(l[i], reinterpret_cast<const uint64_t *>(fs)[32 * h2 + i]);
                 }
-                if (b > 0 && (any || er_new != er) && __all_sync(0xffffffffu, okp)) {
+                if (b > 0 && (any || er_new != er)) {
+                    // O^T: every column for a new exponent, else only those of the heads that moved
                     tc_fence_after();
                     const float fe = exp2f((float)(er - er_new));
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
-                        // heads whose reference stayed need no pass over their columns
-                        if (er_new == er && __all_sync(0xffffffffu, fs[32 * ch + lane] == 1.0f)) continue;
-                        uint32_t o[32];
                         const uint32_t oa = t_lane + C::TMEM_O + 128 * h2 + 32 * ch;
+                        uint32_t moved = __ballot_sync(0xffffffffu, fs[32 * ch + lane] != 1.0f);
+                        if (er_new == er && __popc(moved) <= 4) {
+                            while (moved != 0u) {
+                                const int i = __ffs(moved) - 1;
+                                moved &= moved - 1u;
+                                const uint32_t o = tmem_ld1(oa + i);
+                                tmem_wait_ld();
+                                tmem_st1(oa + i, __float_as_uint(__uint_as_float(o) * fs[32 * ch + i]));
+                            }
+                            continue;
+                        }
+                        uint32_t o[32];
                         tmem_ld32(oa, o);
                         tmem_wait_ld();
 #pragma unroll
@@ -745,36 +778,48 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     tmem_wait_st();
                 }
                 er = er_new;
-                // ---- P'^T of this thread's key for its 64 heads
+                // ---- P'^T of this thread's key for its 64 heads, 16 heads at a time
                 const float kf = vis ? ks * __uint_as_float((uint32_t)min(254 + C::BASE - er, 254) << 23) : 0.f;
+                const uint64_t ks2 = pack_f32x2(ks, ks), kf2 = pack_f32x2(kf, kf);
+                const bool all_vis = __all_sync(0xffffffffu, vis);
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
-                    uint32_t sr[32], hi[8], lo[8];
+                    uint32_t sr[32];
                     tmem_ld32(sb + 32 * jj, sr);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int h = 32 * jj + 2 * i;
-                        const float2 m2 = reinterpret_cast<const float2 *>(mr)[32 * h2 + 16 * jj + i];
-                        const float2 q2 = reinterpret_cast<const float2 *>(qs)[32 * h2 + 16 * jj + i];
-                        const float p0 = vis ? ex2_approx(fmaf(__uint_as_float(sr[2 * i]) * ks, q2.x, -m2.x)) : 0.f;
-                        const float p1 = vis ? ex2_approx(fmaf(__uint_as_float(sr[2 * i + 1]) * ks, q2.y, -m2.y)) : 0.f;
-                        l[h] += p0;
-                        l[h + 1] += p1;
-                        uint32_t hh, ll;
-                        split_e4m3(__floats2half2_rn(p0 * kf, p1 * kf), hh, ll);
-                        hi[i >> 1] = (i & 1) ? hi[i >> 1] | hh << 16 : hh;
-                        lo[i >> 1] = (i & 1) ? lo[i >> 1] | ll << 16 : ll;
-                    }
-#pragma unroll
                     for (int v = 0; v < 2; ++v) {
+                        uint32_t hi[4], lo[4];
+                        float4 w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const float4 *>(mq)[32 * h2 + 16 * jj + 8 * v + i];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint64_t s2 = pack_f32x2(__uint_as_float(sr[16 * v + 2 * i]), __uint_as_float(sr[16 * v + 2 * i + 1]));
+                            const uint64_t z2 = fma3_f32x2(mul_f32x2(s2, ks2), pack_f32x2(w[i].z, w[i].w), pack_f32x2(w[i].x, w[i].y));
+                            float p0, p1;
+                            unpack_f32x2(z2, p0, p1);
+                            p0 = ex2_approx(p0);
+                            p1 = ex2_approx(p1);
+                            if (!all_vis) {
+                                p0 = vis ? p0 : 0.f;
+                                p1 = vis ? p1 : 0.f;
+                            }
+                            const uint64_t p2 = pack_f32x2(p0, p1);
+                            l[16 * jj + 8 * v + i] = add_f32x2(l[16 * jj + 8 * v + i], p2);
+                            unpack_f32x2(mul_f32x2(p2, kf2), p0, p1);
+                            uint32_t hh, ll;
+                            split_e4m3(__floats2half2_rn(p0, p1), hh, ll);
+                            hi[i >> 1] = (i & 1) ? hi[i >> 1] | hh << 16 : hh;
+                            lo[i >> 1] = (i & 1) ? lo[i >> 1] | ll << 16 : ll;
+                        }
                         const uint32_t off = ((2 * jj + v) ^ pswz) << 4;
                         if (h2 == cr) {
-                            st_shared_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
-                            st_shared_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+                            st_shared_v4(ph_row + off, hi[0], hi[1], hi[2], hi[3]);
+                            st_shared_v4(pl_row + off, lo[0], lo[1], lo[2], lo[3]);
                         } else {
-                            st_async_v4(ph_row + off, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3], p_in_peer);
-                            st_async_v4(pl_row + off, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3], p_in_peer);
+                            st_async_v4(ph_row + off, hi[0], hi[1], hi[2], hi[3], p_in_peer);
+                            st_async_v4(pl_row + off, lo[0], lo[1], lo[2], lo[3], p_in_peer);
                         }
                     }
                 }
@@ -784,10 +829,6 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 if (lane == 0) {
                     mbar_arrive_remote(s_free_lead + 8u * (gb & 1));    // S^T consumed
                     if (h2 == cr) mbar_arrive_remote(p_full_lead);      // this warp's 32 rows are in place
-                }
-                if (named_bar_or(1, 256, misc[1] != 0)) {
-                    ok = false;
-                    break;
                 }
             }
             if (!ok && st == 0) abort_pair();
@@ -800,7 +841,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 for (int jj = 0; jj < 2; ++jj) {
                     float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = l[32 * jj + i];
+                    for (int i = 0; i < 16; ++i) unpack_f32x2(l[16 * jj + i], v[2 * i], v[2 * i + 1]);
                     red[quarter * 128 + 64 * h2 + 32 * jj + lane] = mla::transpose_reduce32<false>(v, lane);
                 }
                 named_bar(1, 256);
@@ -817,7 +858,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     fs[h] = okl && l_tot != 0.f ? ue8m0_to_float((uint32_t)(er - C::BASE)) / l_tot : 0.f;
                     if ((h >> 6) == cr) {
                         const float lv =
-                            okl ? (l_tot != 0.f ? (mr[h] + log2f(l_tot)) * 0.6931471805599453f : -INFINITY) : NAN;
+                            okl ? (l_tot != 0.f ? (log2f(l_tot) - mq[mqh]) * 0.6931471805599453f : -INFINITY) : NAN;
                         if (SPLIT) sp.lse_part[pbase + h] = lv;
                         else lse[obase + h] = lv;
                     }
