@@ -37,15 +37,20 @@
 // rows never enters a sum.
 //
 // Probabilities: the reference maximum m[h] moves when a block maximum exceeds it by more than
-// TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and its smallest step 2^-9 is 2^-15 of the
-// largest p.  The sum l takes p itself in fp32.
+// TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and half its smallest step, 2^-10, is 2^-14 of
+// the largest p.  A move costs 1 to 1.5 us (O^T goes through registers): with TAU = 2.8 and
+// BASE = 6 two to three heads of 128 moved in every block of normally distributed scores (a
+// simulation; 621 us for 1024 queries), with TAU = 4.8 one in ten blocks has any.  The sum l takes
+// p itself in fp32.
 //
 // Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
 // prepare (warp 8 also publishes each unit's block count and loads its q: the raw bf16 rows
 // land in q_s and are split in place into hi and lo, each head at its own power of two; then
-// they fetch the scales of the keys of each block, up to four blocks ahead), 12-19 softmax and
-// epilogue: TMEM lane quarter w % 4, head half (w - 12) / 4.
+// they fetch the scales of the keys of each block, up to four blocks ahead, and write the
+// previous unit's output), 12-19 softmax: TMEM lane quarter w % 4, head half (w - 12) / 4.
 #pragma once
+
+#include <type_traits>
 
 #include "cache_write_fp8.cuh"
 #include "dsa_common.cuh"
@@ -63,7 +68,7 @@ struct Cfg {
     static constexpr int NQ = 9;                    // raw: 9 x 64 dims; split: 4 hi, 4 lo, [RoPE hi | lo]
     static constexpr int NSLOT = 7, NLOAD = 7;
     static constexpr int NINFO = 4;                 // blocks of key scales kept ahead
-    static constexpr int NQS = 4;                   // units of q scales kept
+    static constexpr int NQS = 3;                   // units of q scales kept
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_PH = OFF_Q + NQ * QATOM;           // P' hi [256 keys][64 heads]
     static constexpr int OFF_PL = OFF_PH + 256 * 64;            // P' lo
@@ -72,24 +77,26 @@ struct Cfg {
     static constexpr int OFF_XM = OFF_RED + 4 * 128 * 4;        // [2][128] f32, peer block maxima
     static constexpr int OFF_XL = OFF_XM + 2 * 128 * 4;         // [128] f32, peer row sums
     static constexpr int OFF_MQ = OFF_XL + 128 * 4;             // [64] {-m, -m', qs, qs'} of a head pair
-    static constexpr int OFF_FS = OFF_MQ + 64 * 16;             // [128] f32, rescale factor / output factor
+    static constexpr int OFF_FS = OFF_MQ + 64 * 16;             // [128] f32, rescale factor
     static constexpr int OFF_QS = OFF_FS + 128 * 4;             // [NQS][128] f32, 2^f[h] * sm_scale * log2 e
     static constexpr int OFF_INFO = OFF_QS + NQS * 128 * 4;     // [NINFO][128] f32, key scale or -1 (masked)
     static constexpr int OFF_ER = OFF_INFO + NINFO * 128 * 4;   // [NINFO][4] int, running maxima of exponents
-    static constexpr int OFF_BAR = OFF_ER + NINFO * 4 * 4;
+    static constexpr int OFF_FO = OFF_ER + NINFO * 4 * 4;       // [2][128] f32, output factors of a unit
+    static constexpr int OFF_MV = OFF_FO + 2 * 128 * 4;         // [4] u32, heads whose reference moved
+    static constexpr int OFF_BAR = OFF_MV + 16;
     // empty[7] pfull[7] q_raw q_ready q_free s_full[2] s_free[2] p_full pv_done o_ready xbar[2] lbar
-    // drain unit_full[2] unit_free[2] info_full[4] info_free[4] p_in
-    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO + 1;
+    // drain unit_full[2] unit_free[2] info_full[4] info_free[4] p_in fo_full[2] o_free qs_full[3]
+    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO + 1 + 3 + NQS;
     // [0] TMEM base, [1] abort, [2..3] unit blocks, [4..5] unit fallback keys, [6] peer's abort flag
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
     static constexpr int OFF_LASTPOS = OFF_MISC + 32;           // even CTA: [2][NSLOT] last ring position issued
     static constexpr int SMEM = OFF_LASTPOS + 2 * NSLOT * 4;
     static constexpr int PREP0 = 8, SOFT0 = 12, WARPS = 20, THREADS = 32 * WARPS;
-    // of the 640 x 96 registers of the launch: 256 x 56 + 128 x 72 + 256 x 144 = 60,416
-    static constexpr int REG_LOAD = 56, REG_PREP = 72, REG_SOFT = 144;
+    // of the 640 x 96 registers of the launch: 256 x 64 + 128 x 72 + 256 x 136 = 60,416
+    static constexpr int REG_LOAD = 64, REG_PREP = 72, REG_SOFT = 136;
     static constexpr int TMEM_S = 0, TMEM_O = 256;
-    static constexpr float TAU = 2.8f;              // lazy-rescale threshold (log2 units)
-    static constexpr int BASE = 6;                  // 2^(TAU + BASE) = 446 < 448
+    static constexpr float TAU = 4.8f;              // lazy-rescale threshold (log2 units)
+    static constexpr int BASE = 4;                  // 2^(TAU + BASE) = 446 < 448
     static constexpr int ER_MIN = BASE;             // exponent bytes below this count as this
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(NLOAD == NSLOT, "one ring slot per gathering warp");
@@ -190,13 +197,15 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const uint32_t sbase = smem_u32(smem);
     const bool misaligned = (sbase & 1023u) != 0;           // uniform; no unit runs then
     const uint32_t q_s = sbase + C::OFF_Q;
-    const uint32_t ph_s = sbase + C::OFF_PH, pl_s = sbase + C::OFF_PL;
+    const uint32_t ph_s = sbase + C::OFF_PH;
     const uint32_t ring_s = sbase + C::OFF_RING;
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
     float *xm = reinterpret_cast<float *>(smem + C::OFF_XM);
     float *xl = reinterpret_cast<float *>(smem + C::OFF_XL);
     float *mq = reinterpret_cast<float *>(smem + C::OFF_MQ);
     float *fs = reinterpret_cast<float *>(smem + C::OFF_FS);
+    float *fo = reinterpret_cast<float *>(smem + C::OFF_FO);
+    uint32_t *mvw = reinterpret_cast<uint32_t *>(smem + C::OFF_MV);
     float *qsc = reinterpret_cast<float *>(smem + C::OFF_QS);
     float *info = reinterpret_cast<float *>(smem + C::OFF_INFO);
     int *ers = reinterpret_cast<int *>(smem + C::OFF_ER);
@@ -219,6 +228,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     auto info_full = [&](int i) { return q_raw + 144 + 8u * i; };
     auto info_free = [&](int i) { return q_raw + 144 + 8u * (C::NINFO + i); };
     const uint32_t p_in = q_raw + 144 + 8u * (2 * C::NINFO); // P'^T rows of the peer's keys landed here
+    auto fo_full = [&](int i) { return p_in + 8 + 8u * i; }; // a unit's output factors are in place
+    const uint32_t o_free = p_in + 24;                       // even CTA: O^T of both CTAs read out
+    auto qs_full = [&](int i) { return p_in + 32 + 8u * i; };   // a unit's q scales are in place
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
     volatile int *unit_nb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
     volatile int *unit_fb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);
@@ -233,7 +245,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         mbar_init(q_ready, 8);            // 4 preparing warps of each CTA
         mbar_init(q_free, 1);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(s_full(b), 2);      // the MMA thread's own arrival and its commit
+            mbar_init(s_full(b), 1);
             mbar_init(s_free(b), 16);     // 8 softmax warps of each CTA
             mbar_init(xbar(b), 1);
             mbar_init(unit_full(b), 1);   // warp 8
@@ -241,6 +253,10 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         mbar_init(p_full, 9);             // 4 warps of each CTA (own rows), the odd CTA's relay
         mbar_init(p_in, 1);
+        mbar_init(fo_full(0), 4);         // the softmax warps of threads 0 .. 127
+        mbar_init(fo_full(1), 4);
+        mbar_init(o_free, 8);             // 4 preparing warps of each CTA
+        for (int i = 0; i < C::NQS; ++i) mbar_init(qs_full(i), 4);   // own preparing warps (and the peer's bytes)
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(lbar, 1);
@@ -370,7 +386,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (ok) mbar_arrive(unit_free(j & 1));
             for (int b = 0; ok && b < nblocks; ++b, ++gb) {
                 mbar_expect_tx(p_in, 128 * 128);
-                ok = mbar_wait_cluster(p_in, gb & 1) && !misc[1];
+                ok = mbar_wait(p_in, gb & 1) && !misc[1];
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive_remote(p_full_lead);
             }
@@ -385,7 +401,6 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // descriptors step by bytes / 16 in their low word
         const uint64_t dq = desc_sw128(q_s), da_k = desc_sw128(ring_s), da_mn = desc_sw128_mn(ring_s, C::ATOM);
         const uint64_t dph = desc_sw64_mn(ph_s);
-        const uint32_t s_full_peer = mapa_shared(s_full(0), 1);
         bool ok = run;
         bool issued = false;
         int slot = 0, phase = 0;                             // ring slot and its phase
@@ -399,7 +414,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int nblocks = __shfl_sync(0xffffffffu, unit_nb[j & 1], 0);
             if (elect_one()) mbar_arrive(unit_free(j & 1));
             if (nblocks == 0) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(q_ready, nq & 1))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(q_ready, nq & 1))) {
                 ok = false;
                 break;
             }
@@ -437,15 +452,6 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                     if (elect_one()) {
                         if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
-                        // this thread's own arrivals for a unit's first block pass on what it has seen
-                        // (the q scales, through q_ready) to the softmax warps that wait for S^T
-                        if (b == 0) {
-                            mbar_arrive_cluster(s_full(gb & 1));
-                            mbar_arrive_cluster(s_full_peer + 8u * (gb & 1));
-                        } else {
-                            mbar_arrive(s_full(gb & 1));
-                            mbar_arrive_remote(s_full_peer + 8u * (gb & 1));
-                        }
                         mma_commit_pair_both(s_full(gb & 1));
                     }
                     issued = true;
@@ -463,7 +469,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         }
                     }
                     if (elect_one()) mbar_expect_tx(p_in, 128 * 128);
-                    okw = okw && mbar_wait(p_full, gb & 1) && mbar_wait_cluster(p_in, gb & 1);
+                    // the previous unit's O^T has been read out
+                    if (b == 0 && nq > 0) okw = okw && mbar_wait(o_free, (nq - 1) & 1);
+                    okw = okw && mbar_wait(p_full, gb & 1) && mbar_wait(p_in, gb & 1);
                     fence_proxy_async_smem();
                     tc_fence_after();
 #pragma unroll
@@ -507,15 +515,63 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
     } else if (warp < C::SOFT0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_PREP));
-        // ------------------------------------------------ units, q, key scales
+        // ------------------------------------------------ units, q, key scales, output
         const int pw = warp - C::PREP0;
         const float sl2 = P.sm_scale * 1.4426950408889634f;
         const uint32_t q_ready_lead = mapa_shared(q_ready, 0);
         const uint32_t qsc_peer = mapa_shared(sbase + C::OFF_QS, (uint32_t)peer);
+        const uint32_t qs_full_peer = mapa_shared(qs_full(0), (uint32_t)peer);
         if (pw == 0 && lane == 0) prefetch_tmap(&tm_q);
         bool ok = run;
         int gb = 0;                                          // blocks so far
         int nq = 0;                                          // units with blocks so far
+        int nl = 0;                                          // q loads so far
+        int qslot = 0;                                       // where the unit's q scales go
+        // ---- epilogue of a unit (token pt, split ps, the pn-th with blocks): O^T times its output
+        // factors into out.  These warps do it, so that the softmax goes on with the next unit; its
+        // first PV waits for o_free.
+        const uint32_t o_free_lead = mapa_shared(o_free, 0);
+        auto epilogue = [&](int pt, int ps, int pn) {
+            bool fine = mbar_wait(fo_full(pn & 1), (pn >> 1) & 1);
+            fine = mbar_wait(o_ready, pn & 1) && fine;
+            if (!__all_sync(0xffffffffu, fine)) return false;
+            tc_fence_after();
+            const float *f = fo + 128 * (pn & 1);
+            // O^T block i: lanes = value dims 256 i + 128 cr + 32 pw + lane, columns = heads
+            const bool odd = (lane & 1) != 0;
+#pragma unroll 1
+            for (int c8 = 0; c8 < 8; ++c8) {
+                const int i = c8 >> 2, ch = c8 & 3;
+                uint32_t o[32];
+                tmem_ld32(tmem + ((uint32_t)(pw * 32) << 16) + C::TMEM_O + 32 * c8, o);
+                tmem_wait_ld();
+                if (c8 == 7) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(o_free_lead);
+                }
+                if (SPLIT) {   // fp32 partial rows (32 lanes: 128 bytes per head)
+                    float *op = sp.o_part + (((int64_t)pt * nsplit + ps) * 128 + 32 * ch) * 512 + 256 * i + 128 * cr + 32 * pw + lane;
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) op[(int64_t)h * 512] = __uint_as_float(o[h]) * f[32 * ch + h];
+                } else {
+                    // bf16 rows from registers: lanes 2m and 2m + 1 swap one value per head pair, so
+                    // each stores two adjacent dims of one head (64 contiguous bytes per head per warp)
+                    __nv_bfloat16 *orow = out + ((int64_t)pt * 128 + 32 * ch + (odd ? 1 : 0)) * 512 + 256 * i + 128 * cr +
+                                          32 * pw + (lane & ~1);
+#pragma unroll
+                    for (int h = 0; h < 32; h += 2) {
+                        const float2 f2 = reinterpret_cast<const float2 *>(f)[16 * ch + (h >> 1)];
+                        const float v0 = __uint_as_float(o[h]) * f2.x, v1 = __uint_as_float(o[h + 1]) * f2.y;
+                        const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                        const uint32_t w = odd ? pack_bf16x2(recv, v1) : pack_bf16x2(v0, recv);
+                        *reinterpret_cast<uint32_t *>(orow + (int64_t)h * 512) = w;
+                    }
+                }
+            }
+            return true;
+        };
+        int pt = -1, ps = 0;                                 // the unit whose epilogue is due (number nq - 1 or nq - 2)
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
             const int t = T - 1 - u / nsplit;
             const int split = u % nsplit;
@@ -524,6 +580,14 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             int nblocks;
             bool okw = true;
             if (pw == 0) {
+                auto load_q = [&]() {
+                    mbar_expect_tx(q_raw, C::NQ * C::QATOM);
+                    for (int a = 0; a < C::NQ; ++a)
+                        tma_load_2d(q_s + a * C::QATOM, &tm_q, q_raw, 64 * a, t * 128 + 64 * cr);
+                };
+                // The first unit's q goes ahead of the gathers, which would queue before it in the copy
+                // engine (4.3 instead of 2 us); nothing holds q_s yet.
+                if (j == 0 && lane == 0) load_q();
                 const Unit un = unit_scan(P, ri, irow, K, split, bps, lane);
                 nblocks = un.nblocks;
                 if (lane == 0) {
@@ -534,28 +598,23 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         mbar_arrive(unit_full(j & 1));
                     }
                     if (okw && nblocks > 0 && nq > 0) okw = mbar_wait(q_free, (nq - 1) & 1);
-                    if (okw && nblocks > 0) {
-                        mbar_expect_tx(q_raw, C::NQ * C::QATOM);
-                        for (int a = 0; a < C::NQ; ++a)
-                            tma_load_2d(q_s + a * C::QATOM, &tm_q, q_raw, 64 * a, t * 128 + 64 * cr);
-                    }
+                    if (okw && nblocks > 0 && j > 0) load_q();
                 }
+                okw = __shfl_sync(0xffffffffu, okw, 0);
+                nl += (j == 0 || (okw && nblocks > 0)) ? 1 : 0;
             } else {
                 okw = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
                 nblocks = okw ? unit_nb[j & 1] : 0;
                 if (__all_sync(0xffffffffu, okw) && lane == 0) mbar_arrive(unit_free(j & 1));
             }
+            if (pw > 0) nl += (j == 0 || (okw && nblocks > 0)) ? 1 : 0;
+            // every load is waited for, whatever happens to its unit: none is in flight at the end
+            if (j == 0 || nblocks > 0) okw = mbar_wait(q_raw, (nl - 1) & 1) && okw;
             if (!__all_sync(0xffffffffu, okw) || misc[1]) {
-                // (a q load just issued is waited for below the loop)
-                if (pw == 0 && lane == 0 && okw && nblocks > 0) mbar_wait(q_raw, nq & 1);
                 ok = false;
                 break;
             }
             if (nblocks == 0) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait(q_raw, nq & 1))) {
-                ok = false;
-                break;
-            }
             // ---- split q in place: 8 lanes per head row, each the 16-byte chunk g of the row's nine
             // 128-byte lines (dims 64 a + 8 g ..); the split row takes the same nine lines
             const int g8 = lane & 7;
@@ -607,16 +666,21 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     *reinterpret_cast<uint2 *>(line + al * C::QATOM + ((cl ^ (r & 7)) << 4) + 8 * (g8 & 1)) = l;
                 }
                 if (g8 == 0) {
-                    const int at = 128 * (nq & (C::NQS - 1)) + 64 * cr + r;
+                    const int at = 128 * qslot + 64 * cr + r;
                     const float s = ue8m0_to_float(byte) * sl2;
                     qsc[at] = s;
-                    st_cluster_u32(qsc_peer + 4u * at, __float_as_uint(s));
+                    st_async_f32(qsc_peer + 4u * at, s, qs_full_peer + 8u * qslot);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(q_ready_lead);
+            if (lane == 0) {
+                mbar_arrive_remote(q_ready_lead);
+                if (pw == 0) mbar_expect_tx(qs_full(qslot), 64 * 4);   // the scales of the peer's heads
+                else mbar_arrive(qs_full(qslot));
+            }
             ++nq;
+            qslot = qslot == C::NQS - 1 ? 0 : qslot + 1;
             // ---- scales of this CTA's keys (-1: masked) and the running largest exponent over both
             // CTAs' keys, block by block
             const int32_t *irow_s = irow + split * bps * C::BLK;
@@ -646,12 +710,20 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 if (lane == 0) ers[4 * sl + pw] = er;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(info_full(sl));
+                // the softmax has what it needs to start: the previous unit's epilogue
+                if (b == 0 && pt >= 0 && !epilogue(pt, ps, nq - 2)) {
+                    ok = false;
+                    break;
+                }
             }
+            pt = t;
+            ps = split;
         }
+        if (ok && pt >= 0) ok = epilogue(pt, ps, nq - 1);
         if (!ok && lane == 0) abort_pair();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFT));
-        // ------------------------------------------------ softmax + epilogue
+        // ------------------------------------------------ softmax
         const int st = tid - 32 * C::SOFT0;                  // 0 .. 255
         const int quarter = warp & 3;
         const int h2 = (warp - C::SOFT0) >> 2;               // head half handled by this warp
@@ -670,6 +742,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         bool ok = run;
         int gb0 = 0;                                         // blocks of the earlier units
         int nq = 0;                                          // units with blocks so far
+        int qslot = 0, qphase = 0;
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
             const int t = T - 1 - u / nsplit;
             const int split = u % nsplit;
@@ -682,7 +755,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (st == 0) mbar_arrive(unit_free(j & 1));
             const int mqh = (st >> 1) * 4 + (st & 1);        // st < 128: this thread's head in mq
             if (st < 128) mq[mqh] = INFINITY;                // minus the reference maximum
-            const float *qs = qsc + 128 * (nq & (C::NQS - 1));
+            const float *qs = qsc + 128 * qslot;
             uint64_t l[32];                                  // row sums of head pairs
 #pragma unroll
             for (int i = 0; i < 32; ++i) l[i] = 0ull;
@@ -691,8 +764,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const int gb = gb0 + b;
                 const int sl = gb & (C::NINFO - 1);
                 const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
-                                  !(b == 0 ? mbar_wait_cluster(s_full(gb & 1), (gb >> 1) & 1)
-                                           : mbar_wait(s_full(gb & 1), (gb >> 1) & 1));
+                                  (b == 0 && !mbar_wait(qs_full(qslot), qphase)) ||
+                                  !mbar_wait(s_full(gb & 1), (gb >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 const float ks = info[128 * sl + key];
@@ -702,26 +775,35 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 if (lane == 0) mbar_arrive(info_free(sl));
                 const bool vis = !(ks < 0.f);
                 const uint32_t sb = t_lane + C::TMEM_S + 128 * (gb & 1) + 64 * h2;
+                const bool all_vis = __all_sync(0xffffffffu, vis);
                 // ---- block maxima of this CTA's keys (per head), then of the pair
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
                     uint32_t sr[32];
                     tmem_ld32(sb + 32 * jj, sr);
                     tmem_wait_ld();
-                    float mine = -INFINITY;
+                    tmem_regs_ready(sr);
+                    if (!all_vis) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float r = warp_fmax(vis ? __uint_as_float(sr[i]) * ks : -INFINITY);
-                        mine = lane == i ? r : mine;
+                        for (int i = 0; i < 32; ++i) sr[i] = vis ? sr[i] : 0xff800000u;
                     }
-                    red[quarter * 128 + 64 * h2 + 32 * jj + lane] = mine;
+                    const float k1 = vis ? ks : 1.0f;
+                    float4 *r4 = reinterpret_cast<float4 *>(red + quarter * 128 + 64 * h2 + 32 * jj);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float4 r;
+                        r.x = warp_fmax(__uint_as_float(sr[4 * i]) * k1);
+                        r.y = warp_fmax(__uint_as_float(sr[4 * i + 1]) * k1);
+                        r.z = warp_fmax(__uint_as_float(sr[4 * i + 2]) * k1);
+                        r.w = warp_fmax(__uint_as_float(sr[4 * i + 3]) * k1);
+                        if (lane == 0) r4[i] = r;
+                    }
                 }
                 // every exit decision is taken through a barrier, so the 8 warps stay together
                 if (named_bar_or(1, 256, fail)) {
                     ok = false;
                     break;
                 }
-                bool need = false;
                 if (st < 128) {
                     const int h = st;
                     const float m_cta = fmaxf(fmaxf(red[h], red[128 + h]), fmaxf(red[256 + h], red[384 + h]));
@@ -730,50 +812,60 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float q = qs[h];
                     if (b == 0) mq[mqh + 2] = q;
                     const float m_old = -mq[mqh];
-                    const bool okx = mbar_wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
+                    const bool okx = mbar_wait(xbar(gb & 1), (gb >> 1) & 1);
                     const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * q;
-                    need = m_blk > m_old + C::TAU;
-                    fs[h] = (need && m_old != -INFINITY) ? exp2f(m_old - m_blk) : 1.0f;
+                    const bool need = m_blk > m_old + C::TAU;
+                    fs[h] = (need && m_old != -INFINITY) ? ex2_approx(m_old - m_blk) : 1.0f;
                     if (need) mq[mqh] = -m_blk;
                     if (!okx) misc[1] = 1;
+                    const uint32_t w = __ballot_sync(0xffffffffu, need);
+                    if (lane == 0) mvw[warp - C::SOFT0] = b > 0 ? w : 0u;   // warp i: heads 32 i .. + 31
                 }
-                const bool any = named_bar_or(1, 256, need);
-                // PV_{b-1} has read P'^T and, for a rescale, O^T is whole (block 0's predecessor, the
-                // previous unit's last PV, completed before that unit's epilogue)
+                named_bar(1, 256);
+                // the previous PV (this unit's or the last one's) has read P'^T and, for a rescale, O^T is whole
                 bool okp = true;
-                if (b > 0) okp = mbar_wait(pv_done, (gb - 1) & 1);
+                if (gb > 0) okp = mbar_wait(pv_done, (gb - 1) & 1);
                 if (!okp) misc[1] = 1;
                 __syncwarp();
-                if (b > 0 && any) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        l[i] = mul_f32x2(l[i], reinterpret_cast<const uint64_t *>(fs)[32 * h2 + i]);
-                }
-                if (b > 0 && (any || er_new != er)) {
-                    // O^T: every column for a new exponent, else only those of the heads that moved
+                const uint4 mv = *reinterpret_cast<const uint4 *>(mvw);
+                if ((mv.x | mv.y | mv.z | mv.w) != 0u || (b > 0 && er_new != er)) {
                     tc_fence_after();
-                    const float fe = exp2f((float)(er - er_new));
-#pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        const uint32_t oa = t_lane + C::TMEM_O + 128 * h2 + 32 * ch;
-                        uint32_t moved = __ballot_sync(0xffffffffu, fs[32 * ch + lane] != 1.0f);
-                        if (er_new == er && __popc(moved) <= 4) {
-                            while (moved != 0u) {
-                                const int i = __ffs(moved) - 1;
-                                moved &= moved - 1u;
-                                const uint32_t o = tmem_ld1(oa + i);
-                                tmem_wait_ld();
-                                tmem_st1(oa + i, __float_as_uint(__uint_as_float(o) * fs[32 * ch + i]));
+                    // the row sums of this warp's heads, 16 at a time
+                    const uint32_t own[2] = {h2 ? mv.z : mv.x, h2 ? mv.w : mv.y};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if ((own[c >> 1] >> (16 * (c & 1)) & 0xffffu) != 0u) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 w = reinterpret_cast<const float4 *>(fs)[16 * h2 + 4 * c + i];
+                                l[8 * c + 2 * i] = mul_f32x2(l[8 * c + 2 * i], pack_f32x2(w.x, w.y));
+                                l[8 * c + 2 * i + 1] = mul_f32x2(l[8 * c + 2 * i + 1], pack_f32x2(w.z, w.w));
                             }
-                            continue;
                         }
-                        uint32_t o[32];
-                        tmem_ld32(oa, o);
+                    }
+                    // O^T: every column for a new exponent, else the groups of 16 heads with one that moved
+                    const uint32_t oa = t_lane + C::TMEM_O + 128 * h2;
+                    const float fe = exp2f((float)(er - er_new));
+                    uint32_t groups = ((mv.x & 0xffffu) ? 1u : 0u) | ((mv.x >> 16) ? 2u : 0u) | ((mv.y & 0xffffu) ? 4u : 0u) |
+                                      ((mv.y >> 16) ? 8u : 0u) | ((mv.z & 0xffffu) ? 16u : 0u) | ((mv.z >> 16) ? 32u : 0u) |
+                                      ((mv.w & 0xffffu) ? 64u : 0u) | ((mv.w >> 16) ? 128u : 0u);
+                    if (er_new != er) groups = 255u;
+#pragma unroll 1
+                    while (groups != 0u) {
+                        const int c = __ffs(groups) - 1;
+                        groups &= groups - 1u;
+                        uint32_t o[16];
+                        tmem_ld16(oa + 16 * c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * (fs[32 * ch + i] * fe));
-                        tmem_st32(oa, o);
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = reinterpret_cast<const float4 *>(fs)[4 * c + i];
+                            o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * (f.x * fe));
+                            o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * (f.y * fe));
+                            o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * (f.z * fe));
+                            o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * (f.w * fe));
+                        }
+                        tmem_st16(oa + 16 * c, o);
                     }
                     tmem_wait_st();
                 }
@@ -781,48 +873,48 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 // ---- P'^T of this thread's key for its 64 heads, 16 heads at a time
                 const float kf = vis ? ks * __uint_as_float((uint32_t)min(254 + C::BASE - er, 254) << 23) : 0.f;
                 const uint64_t ks2 = pack_f32x2(ks, ks), kf2 = pack_f32x2(kf, kf);
-                const bool all_vis = __all_sync(0xffffffffu, vis);
+                auto probabilities = [&](auto masked) {
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    uint32_t sr[32];
-                    tmem_ld32(sb + 32 * jj, sr);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        uint32_t hi[4], lo[4];
-                        float4 w[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const float4 *>(mq)[32 * h2 + 16 * jj + 8 * v + i];
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t sr[16], hi[8], lo[8];
+                        tmem_ld16(sb + 16 * v, sr);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint64_t s2 = pack_f32x2(__uint_as_float(sr[16 * v + 2 * i]), __uint_as_float(sr[16 * v + 2 * i + 1]));
-                            const uint64_t z2 = fma3_f32x2(mul_f32x2(s2, ks2), pack_f32x2(w[i].z, w[i].w), pack_f32x2(w[i].x, w[i].y));
+                            const float4 w = reinterpret_cast<const float4 *>(mq)[32 * h2 + 8 * v + i];
+                            const uint64_t s2 = pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+                            const uint64_t z2 = fma3_f32x2(mul_f32x2(s2, ks2), pack_f32x2(w.z, w.w), pack_f32x2(w.x, w.y));
                             float p0, p1;
                             unpack_f32x2(z2, p0, p1);
                             p0 = ex2_approx(p0);
                             p1 = ex2_approx(p1);
-                            if (!all_vis) {
+                            if (masked.value) {
                                 p0 = vis ? p0 : 0.f;
                                 p1 = vis ? p1 : 0.f;
                             }
                             const uint64_t p2 = pack_f32x2(p0, p1);
-                            l[16 * jj + 8 * v + i] = add_f32x2(l[16 * jj + 8 * v + i], p2);
+                            l[8 * v + i] = add_f32x2(l[8 * v + i], p2);
                             unpack_f32x2(mul_f32x2(p2, kf2), p0, p1);
-                            uint32_t hh, ll;
-                            split_e4m3(__floats2half2_rn(p0, p1), hh, ll);
-                            hi[i >> 1] = (i & 1) ? hi[i >> 1] | hh << 16 : hh;
-                            lo[i >> 1] = (i & 1) ? lo[i >> 1] | ll << 16 : ll;
+                            split_e4m3(__floats2half2_rn(p0, p1), hi[i], lo[i]);
                         }
-                        const uint32_t off = ((2 * jj + v) ^ pswz) << 4;
+                        uint32_t h[4], g[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            h[i] = __byte_perm(hi[2 * i], hi[2 * i + 1], 0x5410);
+                            g[i] = __byte_perm(lo[2 * i], lo[2 * i + 1], 0x5410);
+                        }
+                        const uint32_t off = (v ^ pswz) << 4;
                         if (h2 == cr) {
-                            st_shared_v4(ph_row + off, hi[0], hi[1], hi[2], hi[3]);
-                            st_shared_v4(pl_row + off, lo[0], lo[1], lo[2], lo[3]);
+                            st_shared_v4(ph_row + off, h[0], h[1], h[2], h[3]);
+                            st_shared_v4(pl_row + off, g[0], g[1], g[2], g[3]);
                         } else {
-                            st_async_v4(ph_row + off, hi[0], hi[1], hi[2], hi[3], p_in_peer);
-                            st_async_v4(pl_row + off, lo[0], lo[1], lo[2], lo[3], p_in_peer);
+                            st_async_v4(ph_row + off, h[0], h[1], h[2], h[3], p_in_peer);
+                            st_async_v4(pl_row + off, g[0], g[1], g[2], g[3], p_in_peer);
                         }
                     }
-                }
+                };
+                if (all_vis) probabilities(std::false_type{});
+                else probabilities(std::true_type{});
                 tc_fence_before();
                 if (h2 == cr) fence_proxy_async_smem();
                 __syncwarp();
@@ -833,7 +925,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
             if (!ok && st == 0) abort_pair();
 
-            // ---- epilogue: row sums of the pair, lse, O^T / l transposed into out
+            // ---- row sums of the pair: lse, and the output factors for the epilogue
             const int64_t obase = (int64_t)t * 128;
             const int64_t pbase = ((int64_t)t * nsplit + split) * 128;   // partial rows (split mode)
             if (nblocks > 0 && ok) {
@@ -851,58 +943,21 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     st_async_f32(mapa_shared(sbase + C::OFF_XL + 4u * h, (uint32_t)peer), l_cta,
                                  mapa_shared(lbar, (uint32_t)peer));
                     if (st == 0) mbar_expect_tx(lbar, 128 * 4);
-                    const bool okl = mbar_wait_cluster(lbar, nq & 1);
+                    const bool okl = mbar_wait(lbar, nq & 1);
                     // the two CTAs add the same two numbers in the same order
                     const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
                     // O^T holds sum p 2^(e - er + BASE) code
-                    fs[h] = okl && l_tot != 0.f ? ue8m0_to_float((uint32_t)(er - C::BASE)) / l_tot : 0.f;
+                    fo[128 * (nq & 1) + h] =
+                        !okl ? NAN : (l_tot != 0.f ? ue8m0_to_float((uint32_t)(er - C::BASE)) / l_tot : 0.f);
                     if ((h >> 6) == cr) {
                         const float lv =
                             okl ? (l_tot != 0.f ? (log2f(l_tot) - mq[mqh]) * 0.6931471805599453f : -INFINITY) : NAN;
                         if (SPLIT) sp.lse_part[pbase + h] = lv;
                         else lse[obase + h] = lv;
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fo_full(nq & 1));
                 }
-                const bool oko = mbar_wait(o_ready, nq & 1);
-                named_bar(1, 256);
-                tc_fence_after();
-                // O^T block i = h2: lanes = value dims 256 h2 + 128 cr + quarter*32 + lane, columns = heads
-                if (SPLIT) {   // fp32 partial rows, written from registers (32 lanes: 128 bytes per head)
-                    float *op = sp.o_part + pbase * 512 + 256 * h2 + 128 * cr + key;
-#pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + C::TMEM_O + 128 * h2 + 32 * ch, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int h = 32 * ch + i;
-                            op[(int64_t)h * 512] = oko ? __uint_as_float(o[i]) * fs[h] : NAN;
-                        }
-                    }
-                } else {
-                    // bf16 rows from registers: lanes 2m and 2m + 1 swap one value per head pair, so
-                    // each stores two adjacent dims of one head (64 contiguous bytes per head per warp)
-                    const bool odd = (lane & 1) != 0;
-                    __nv_bfloat16 *orow = out + obase * 512 + 256 * h2 + 128 * cr + 32 * quarter + (lane & ~1);
-#pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + C::TMEM_O + 128 * h2 + 32 * ch, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const int h = 32 * ch + i;
-                            const float v0 = oko ? __uint_as_float(o[i]) * fs[h] : NAN;
-                            const float v1 = oko ? __uint_as_float(o[i + 1]) * fs[h + 1] : NAN;
-                            const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                            const uint32_t w = odd ? pack_bf16x2(recv, v1) : pack_bf16x2(v0, recv);
-                            *reinterpret_cast<uint32_t *>(orow + (int64_t)(h + (odd ? 1 : 0)) * 512) = w;
-                        }
-                    }
-                }
-                // O^T read out: ordered before this warp's next arrivals (s_free, p_full) by the
-                // tcgen05 fence that precedes them
             } else {
                 // no visible slot: out = 0, lse = -inf (an aborted pipeline: NaN)
                 const uint32_t fill = nblocks == 0 ? 0u : 0x7fc07fc0u;
@@ -925,7 +980,13 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 }
             }
             gb0 += nblocks;
-            if (nblocks > 0) ++nq;
+            if (nblocks > 0) {
+                ++nq;
+                if (++qslot == C::NQS) {
+                    qslot = 0;
+                    qphase ^= 1;
+                }
+            }
         }
     }
     // ---- teardown: nothing of either CTA is in flight past this point.  After an abort

@@ -404,7 +404,7 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * Accuracy: q and the probabilities enter the tensor cores as two e4m3 numbers each (8
  * significant bits), products are exact and sums are fp32.  A probability is held relative to
  * the largest scale among the keys its row has read so far: next to keys whose scale is 2^n
- * times its own, a key keeps 2^-16 of the largest probability's weight times 2^n.
+ * times its own, a key keeps 2^-14 of the largest probability's weight times 2^n.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd
  *   workspace : device, >= dsa_sparse_mla_fp8_workspace_size(p) bytes, 256-byte aligned (may
  *               be NULL when that is 0).  It holds the parts of rows that are split over

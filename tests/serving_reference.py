@@ -146,10 +146,12 @@ def attention(q, key_rows, values, scale_bytes, sm_scale):
     dzmax = dz.max(1, keepdims=True)
     lse_tol = dzmax[:, 0] + 2.0 ** -20 + 2.0 ** -23 * np.abs(m[:, 0] + np.log(l[:, 0]))
     # (3) p as two e4m3 numbers: relative 2^-8 (4 + 4 significant bits; 2^-12 for the fp16 step
-    #     between), or half the smallest step: 2^-16 of the row's largest p, times the ratio of the
-    #     largest scale to the key's.
+    #     between), or half the smallest step.  p is held as p * 2^(4 + its scale's exponent less the
+    #     largest one) relative to a reference that no p' of the row is below 1 against, and e4m3
+    #     steps by 2^-9 at the least: 2^-10 / 2^4 = 2^-14 of the row's largest p, times the ratio of
+    #     the largest scale to the key's.
     s = 2.0 ** (scale_bytes[key_rows].astype(np.float64) - 127)
-    dp = p * (2.0 ** -8 + 2.0 ** -12 + 2 * dzmax) + 2.0 ** -16 * (s.max() / s)[None, :]
+    dp = p * (2.0 ** -8 + 2.0 ** -12 + 2 * dzmax) + 2.0 ** -14 * (s.max() / s)[None, :]
     # (4) the sums over keys in fp32, and the one rounding to bf16.
     av = np.abs(kv[:, :512])
     out_tol = (dp @ av + 128 * 2.0 ** -23 * (p @ av)) / l + 2.0 ** -8 * np.abs(out) + 2.0 ** -30
