@@ -318,14 +318,30 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _same_device(first: torch.Tensor, *rest) -> None:
-    """Every tensor on the first one's device, and that device current: the launch goes to the
-    current device, and a stream of another one would not order it."""
-    _need(first.is_cuda, "libdsa takes device tensors only")
-    dev = first.device
-    for t in rest:
-        _need(t is None or t.device == dev, "libdsa takes tensors of one device")
-    _need(dev.index == torch.cuda.current_device(), "the tensors' device must be the current device")
+def _addresses(where: str, *tensors_and_types):
+    """Addresses of contiguous tensors of the given types (None: no tensor), all on the current
+    device: the launch goes there, and a stream of another device would not order it."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None   # None: no tensor's device
+    for t, dtype in tensors_and_types:
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous()):
+            raise ValueError(f"{where}: expected a contiguous {dtype} tensor on the current CUDA device, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    return [None if t is None else t.data_ptr() for t, _ in tensors_and_types]
+
+
+# The current stream's handle without the Stream object around it (3 us of a call's 13)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _current_raw_stream(torch.cuda.current_device())
+
+
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 
 
 def dsa_paged_plan(len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts, n_pages: int,
@@ -334,18 +350,14 @@ def dsa_paged_plan(len_cached, len_new, block_table, free_pages, cu_q, cu_k, pos
     lengths (see include/dsa.h).  ``positions`` and ``rows`` may be longer than the step's
     tokens (padding gets position 0 and row -1); ``counts`` [4] receives the new tokens, the
     pages taken, the longest sequence and the error bits."""
-    _same_device(len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts, free_head)
-    tensors = (len_cached, len_new, block_table, free_pages, cu_q, cu_k, positions, rows, counts)
-    _need(all(t.dtype == torch.int32 for t in tensors) and (free_head is None or free_head.dtype == torch.int32),
-          "dsa_paged_plan takes int32 tensors")
+    a = _addresses("dsa_paged_plan", (len_cached, _I32), (len_new, _I32), (block_table, _I32), (free_pages, _I32),
+                   (free_head, _I32), (cu_q, _I32), (cu_k, _I32), (positions, _I32), (rows, _I32), (counts, _I32))
     B, T = len_cached.numel(), positions.numel()
     _need(len_new.numel() == B and cu_q.numel() == B + 1 and cu_k.numel() == B + 1 and counts.numel() == 4
           and rows.numel() == T and block_table.dim() == 2 and block_table.shape[0] == B
           and (free_head is None or free_head.numel() == 1), "dsa_paged_plan: shapes do not agree")
-    lib = load()
-    _check(lib.dsa_paged_plan(B, _ptr(len_cached), _ptr(len_new), _ptr(block_table), block_table.shape[1],
-                              _ptr(free_pages), free_pages.numel(), _ptr(free_head), n_pages, _ptr(cu_q), _ptr(cu_k),
-                              _ptr(positions), _ptr(rows), T, _ptr(counts), _stream(stream)), "dsa_paged_plan")
+    _check(load().dsa_paged_plan(B, a[0], a[1], a[2], block_table.shape[1], a[3], free_pages.numel(), a[4], n_pages, a[5],
+                                 a[6], a[7], a[8], T, a[9], _raw_stream(stream)), "dsa_paged_plan")
 
 
 _ROPE_TYPES = {torch.bfloat16: DSA_ROPE_BF16, torch.float16: DSA_ROPE_FP16, torch.float32: DSA_ROPE_FP32}
@@ -356,19 +368,21 @@ def dsa_rope(x, positions, inv_freq, out, layout: int = DSA_ROPE_INTERLEAVED, ro
     """Rotary positions on dims ``rope_begin .. + rope_dim`` of ``x`` [tokens, heads, head_dim]
     into ``out`` (same shape and type; ``out`` may be ``x``).  Both may be slices of wider
     tensors: only the last dimension has to be dense."""
-    _same_device(x, positions, inv_freq, out)
+    a = _addresses("dsa_rope", (positions, _I32), (inv_freq, _F32))
+    dev = positions.get_device()
+    _need(x.get_device() == dev and out.get_device() == dev, "dsa_rope: every tensor must be on the current CUDA device")
     _need(x.dim() == 3 and x.shape == out.shape, "dsa_rope takes x and out [tokens, heads, head_dim]")
-    _need(x.dtype in _ROPE_TYPES and out.dtype == x.dtype, "dsa_rope takes bf16, fp16 or fp32, the same for x and out")
+    dtype = _ROPE_TYPES.get(x.dtype)
+    _need(dtype is not None and out.dtype is x.dtype, "dsa_rope takes bf16, fp16 or fp32, the same for x and out")
     T, H, D = x.shape
+    xs, os_ = x.stride(), out.stride()
     if rope_dim is None:
         rope_dim = D - rope_begin
-    _need((x.stride(2) == 1 and out.stride(2) == 1) or D == 1, "dsa_rope: the last dimension must be dense")
-    _need(positions.dtype == torch.int32 and positions.numel() == T, "dsa_rope: positions must be int32 [tokens]")
-    _need(inv_freq.dtype == torch.float32 and 2 * inv_freq.numel() == rope_dim, "dsa_rope: inv_freq must be fp32 [rope_dim / 2]")
-    r = DsaRope(T, H, D, rope_begin, rope_dim, layout, _ROPE_TYPES[x.dtype], x.stride(0), x.stride(1), out.stride(0),
-                out.stride(1), scale, 1 if transposed else 0)
-    _check(load().dsa_rope(ctypes.byref(r), ctypes.c_void_p(x.data_ptr()), _ptr(positions), _ptr(inv_freq),
-                           ctypes.c_void_p(out.data_ptr()), _stream(stream)), "dsa_rope")
+    _need(xs[2] == 1 and os_[2] == 1 or D == 1, "dsa_rope: the last dimension must be dense")
+    _need(positions.numel() == T, "dsa_rope: positions must be int32 [tokens]")
+    _need(2 * inv_freq.numel() == rope_dim, "dsa_rope: inv_freq must be fp32 [rope_dim / 2]")
+    r = DsaRope(T, H, D, rope_begin, rope_dim, layout, dtype, xs[0], xs[1], os_[0], os_[1], scale, 1 if transposed else 0)
+    _check(load().dsa_rope(ctypes.byref(r), x.data_ptr(), a[0], a[1], out.data_ptr(), _raw_stream(stream)), "dsa_rope")
 
 
 def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: float = 4096.0,
@@ -382,33 +396,30 @@ def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1
     return freq, att.value
 
 
+_KEY_TYPES = {DSA_BF16: (torch.bfloat16, None), DSA_E4M3: (torch.uint8, torch.float32), DSA_E4M3_UE8M0: (torch.uint8, torch.uint8)}
+
+
 def dsa_cache_write_fp8(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache,
                         k_scale_cache, kv_cache, kv_scale_cache, idx_dtype: int = DSA_E4M3_UE8M0, eps: float = 1e-6,
                         stream=None) -> None:
     """dsa_cache_write into an 8-bit cache: the indexer key as ``idx_dtype`` says, the latent as
     640 e4m3 codes and one ue8m0 scale per row (see include/dsa.h)."""
     n = positions.numel()
-    _same_device(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache, k_scale_cache,
-                 kv_cache, kv_scale_cache)
-    key, scale = {DSA_BF16: (torch.bfloat16, None), DSA_E4M3: (torch.uint8, torch.float32),
-                  DSA_E4M3_UE8M0: (torch.uint8, torch.uint8)}.get(idx_dtype, (None, None))
+    key, scale = _KEY_TYPES.get(idx_dtype, (None, None))
     _need(key is not None, "dsa_cache_write_fp8: idx_dtype must be DSA_BF16, DSA_E4M3 or DSA_E4M3_UE8M0")
-    _need(k_idx_raw.dtype == torch.bfloat16 and kv_raw.dtype == torch.bfloat16 and k_idx_raw.numel() == 128 * n
-          and kv_raw.numel() == 576 * n, "dsa_cache_write_fp8: k_idx_raw must be bf16 [n, 128], kv_raw bf16 [n, 576]")
-    _need(positions.dtype == torch.int32 and rows.dtype == torch.int32 and rows.numel() == n,
-          "dsa_cache_write_fp8: positions and rows must be int32 [n]")
-    _need(all(w.dtype == torch.float32 and w.numel() == m for w, m in
-              ((k_norm_w, 128), (k_norm_b, 128), (kv_norm_w, 512), (inv_freq, 32))),
-          "dsa_cache_write_fp8: k_norm_w, k_norm_b fp32 [128], kv_norm_w fp32 [512], inv_freq fp32 [32]")
-    _need(k_idx_cache.dtype == key and k_idx_cache.shape[-1] == 128 and kv_cache.dtype == torch.uint8
-          and kv_cache.shape[-1] == 640 and kv_scale_cache.dtype == torch.uint8
-          and kv_scale_cache.numel() * 640 == kv_cache.numel(), "dsa_cache_write_fp8: cache types or shapes")
-    _need(k_scale_cache is None if scale is None else k_scale_cache is not None and k_scale_cache.dtype == scale
-          and k_scale_cache.numel() * 128 == k_idx_cache.numel(), "dsa_cache_write_fp8: k_scale_cache does not fit idx_dtype")
-    _check(load().dsa_cache_write_fp8(n, _ptr(k_idx_raw), _ptr(kv_raw), _ptr(positions), _ptr(rows), _ptr(k_norm_w),
-                                      _ptr(k_norm_b), _ptr(kv_norm_w), _ptr(inv_freq), eps, idx_dtype, _ptr(k_idx_cache),
-                                      _ptr(k_scale_cache), _ptr(kv_cache), _ptr(kv_scale_cache), _stream(stream)),
-           "dsa_cache_write_fp8")
+    _need((k_scale_cache is None) == (scale is None), "dsa_cache_write_fp8: k_scale_cache does not fit idx_dtype")
+    a = _addresses("dsa_cache_write_fp8", (k_idx_raw, _BF16), (kv_raw, _BF16), (positions, _I32), (rows, _I32), (k_norm_w, _F32),
+                   (k_norm_b, _F32), (kv_norm_w, _F32), (inv_freq, _F32), (k_idx_cache, key), (k_scale_cache, scale),
+                   (kv_cache, _U8), (kv_scale_cache, _U8))
+    _need(rows.numel() == n and k_idx_raw.numel() == 128 * n and kv_raw.numel() == 576 * n,
+          "dsa_cache_write_fp8: k_idx_raw [n, 128], kv_raw [n, 576], positions and rows [n]")
+    _need(k_norm_w.numel() == 128 and k_norm_b.numel() == 128 and kv_norm_w.numel() == 512 and inv_freq.numel() == 32,
+          "dsa_cache_write_fp8: k_norm_w, k_norm_b [128], kv_norm_w [512], inv_freq [32]")
+    _need(k_idx_cache.shape[-1] == 128 and kv_cache.shape[-1] == 640
+          and kv_scale_cache.numel() * 640 == kv_cache.numel()
+          and (scale is None or k_scale_cache.numel() * 128 == k_idx_cache.numel()), "dsa_cache_write_fp8: cache shapes")
+    _check(load().dsa_cache_write_fp8(n, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], eps, idx_dtype, a[8], a[9], a[10],
+                                      a[11], _raw_stream(stream)), "dsa_cache_write_fp8")
 
 
 def dsa_sparse_mla_fp8_workspace_size(p: DsaProblem) -> int:
@@ -417,17 +428,15 @@ def dsa_sparse_mla_fp8_workspace_size(p: DsaProblem) -> int:
 
 def dsa_sparse_mla_fp8_fwd(p: DsaProblem, q, kv, kv_scale, idx, out, lse, workspace=None, stream=None) -> None:
     """dsa_sparse_mla_fwd over the 8-bit latent cache (kv uint8 [S, 640], kv_scale uint8 [S])."""
-    _same_device(q, kv, kv_scale, idx, out, lse, workspace)
-    T = p.total_q
-    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16 and lse.dtype == torch.float32
-          and idx.dtype == torch.int32 and kv.dtype == torch.uint8 and kv_scale.dtype == torch.uint8,
-          "dsa_sparse_mla_fp8_fwd: q, out bf16, lse fp32, idx int32, kv and kv_scale uint8")
+    a = _addresses("dsa_sparse_mla_fp8_fwd", (q, _BF16), (kv, _U8), (kv_scale, _U8), (idx, _I32), (out, _BF16), (lse, _F32),
+                   (workspace, _U8))
+    T, S = p.total_q, p.total_k
     _need(q.numel() == T * 128 * 576 and out.numel() == T * 128 * 512 and lse.numel() == T * 128
-          and idx.numel() == T * p.topk and kv.numel() >= p.total_k * 640 and kv_scale.numel() >= p.total_k,
+          and idx.numel() == T * p.topk and kv.numel() >= S * 640 and kv_scale.numel() >= S,
           "dsa_sparse_mla_fp8_fwd: shapes do not fit the problem")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().dsa_sparse_mla_fp8_fwd(ctypes.byref(p), _ptr(q), _ptr(kv), _ptr(kv_scale), _ptr(idx), _ptr(out),
-                                         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), "dsa_sparse_mla_fp8_fwd")
+    _check(load().dsa_sparse_mla_fp8_fwd(ctypes.byref(p), a[0], a[1], a[2], a[3], a[4], a[5], a[6],
+                                         0 if workspace is None else workspace.numel(), _raw_stream(stream)),
+           "dsa_sparse_mla_fp8_fwd")
 
 
 def dsa_set_debug_checks(enable: bool) -> None:

@@ -798,16 +798,24 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *po
     dsa::rope::Args a{x, out, positions, inv_freq, r->n_tokens, r->n_heads, r->head_dim, r->rope_begin, r->rope_dim,
                       r->x_token_stride, r->x_head_stride, r->out_token_stride, r->out_head_stride, r->scale,
                       r->transposed != 0, in_place, 1};
-    // tokens per CTA: about four vectors per thread
+    // items (vectors, pairs or copied elements) of a head
     const int64_t per_head = vec ? (il ? r->rope_dim : r->rope_dim / 2) / v + (in_place ? 0 : (r->head_dim - r->rope_dim) / v)
                                  : r->rope_dim / 2 + (in_place ? 0 : r->head_dim - r->rope_dim);
-    int64_t nt = 4 * dsa::rope::NT / (per_head * r->n_heads);
+    const int64_t per_token = per_head * r->n_heads;
+    // tokens per CTA: about four items per thread, or up to eight tokens where that still leaves a
+    // full grid (8192 tokens x 128 heads x 64 dims: 102 us with one, 58 us with four); no more
+    // than the angle table holds
+    int64_t nt = 4 * dsa::rope::NT / per_token;
+    int64_t full = r->n_tokens / dsa::rope::FULL_GRID;
+    full = full < 8 ? full : 8;
+    nt = nt > full ? nt : full;
     const int64_t fit = dsa::rope::MAX_PAIRS / (r->rope_dim / 2);
     nt = nt < fit ? nt : fit;
     nt = nt < dsa::rope::MAX_TOKENS ? nt : dsa::rope::MAX_TOKENS;
     a.tokens_per_cta = nt > 1 ? (int)nt : 1;
     const unsigned grid = (unsigned)(((int64_t)r->n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta);
-    auto launch = [&](auto kernel) { kernel<<<grid, dsa::rope::NT, 0, (cudaStream_t)stream>>>(a); };
+    const unsigned block = (unsigned)(per_token < dsa::rope::NT ? (per_token + 31) / 32 * 32 : dsa::rope::NT);
+    auto launch = [&](auto kernel) { kernel<<<grid, block, 0, (cudaStream_t)stream>>>(a); };
     if (r->dtype == DSA_ROPE_FP32) {
         if (vec) il ? launch(dsa::rope::rope_kernel<float, 4, true>) : launch(dsa::rope::rope_kernel<float, 4, false>);
         else il ? launch(dsa::rope::rope_kernel<float, 1, true>) : launch(dsa::rope::rope_kernel<float, 1, false>);

@@ -10,8 +10,13 @@
 // HBM-bound: every rotated element is read and written once.  Angles, cosines and sines are
 // taken in fp64 (at position 163,840 an fp32 angle is off by 2^-7 rad) once per token and
 // pair, times scale rounded to fp32 in shared memory; the heads of the token share them.  A
-// CTA takes the heads of a few tokens, so that its 256 threads have about four 16-byte
-// vectors each; their loads are issued before the angles are evaluated.
+// CTA takes whole tokens: one each when there are few, several where that still leaves a full
+// grid, so that all its warps evaluate angles at once and then stream without another barrier.
+// A thread keeps its place within a head (one 16-byte vector, its pairs' cosines and sines in
+// registers) and goes from head to head by adding strides: placing each vector by divisions
+// cost more instructions (177 a vector) than rotating it.
+// 8192 tokens x 128 heads x 64 dims out of [.., 192] rows into [.., 576] rows (268 MB, 41 us at
+// the copy bandwidth): 59 to 65 us; 5003 x 64 heads of 128 dims, all copied: 40 us (164 MB, 25 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -24,6 +29,7 @@ namespace rope {
 constexpr int NT = 256;
 constexpr int MAX_PAIRS = 512;       // (cos, sin) pairs kept per CTA
 constexpr int MAX_TOKENS = 16;       // tokens per CTA
+constexpr int FULL_GRID = 148 * 8;   // CTAs that keep every SM busy
 
 struct Args {
     const void *x;
@@ -51,98 +57,105 @@ struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 
+// 16-byte vectors are written as streamed (first to leave L2): 5 to 13 % faster at 50 MB and 134 MB.
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const Vec<T, V> &v) {
+    if constexpr (sizeof(v) == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&v));
+    else *reinterpret_cast<Vec<T, V> *>(p) = v;
+}
+
 // A work item of a head is a rotation (V pairs in the half layout, V / 2 pairs of one vector
 // in the interleaved one, one pair where V = 1) or the copy of V elements outside the
-// rotated part.
+// rotated part.  Threads beyond a whole number of heads idle; the launch sizes the block by the
+// items of a token.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(NT) rope_kernel(Args g) {
-    constexpr int PER = IL ? (V == 1 ? 1 : V / 2) : V;   // pairs of a rotation item
-    constexpr int UNROLL = 4;
-    __shared__ float2 cs[MAX_PAIRS];
+__global__ void __launch_bounds__(NT, !IL && V > 1 ? 5 : 1) rope_kernel(Args g) {
+    constexpr int PER = IL ? (V == 1 ? 1 : V / 2) : V;       // pairs of a rotation item
+    constexpr bool TWO = !IL || V == 1;                      // an item has a second vector
+    // heads in flight per thread (8192 x 128 interleaved: 62 us with 4, 65 with 2; 5003 x 64 half
+    // layout: 45 us with 1 and at most 51 registers, 50 with 1 and 62, 57 to 73 with 2)
+    constexpr int U = V == 1 ? 2 : IL ? 4 : 1;
+    using VT = Vec<T, V>;
+    __shared__ __align__(16) float2 cs[MAX_PAIRS];
+    const int threads = (int)blockDim.x;
     const int half = g.dim >> 1;
     const int64_t t0 = (int64_t)blockIdx.x * g.tokens_per_cta;
     const int nt = (int)min((int64_t)g.tokens_per_cta, g.n_tokens - t0);
     const int rot = half / PER;                              // rotation items of a head
-    const int cop = g.in_place ? 0 : (g.head_dim - g.dim) / V;
-    const int per_head = rot + cop, per_token = per_head * g.n_heads;
-    const int items = per_token * nt;
-    const T *x = static_cast<const T *>(g.x);
-    T *out = static_cast<T *>(g.out);
+    const int per_head = rot + (g.in_place ? 0 : (g.head_dim - g.dim) / V);
+    // thread -> place within a head and first head; heads h0, h0 + step, h0 + 2 step, ..
+    const int kp = min(per_head, threads), step = threads / kp;
+    const int k0 = (int)threadIdx.x % kp, h0 = (int)threadIdx.x / kp;
+    const int heads = h0 < step ? g.n_heads - h0 : 0;        // head h0 + i exists for i < heads
+    const int rounds = (g.n_heads + U * step - 1) / (U * step);
+    const int64_t xs = step * g.x_head, os = step * g.out_head;
 
-    struct Where {
-        int64_t xi, oi;    // element offsets of the head's row
-        int d, dp, pair;   // first dim, partner dim (half layout), index into cs (-1: a copy)
-    };
-    auto where = [&](int i) {
-        const int t = i / per_token, r = i - t * per_token;
-        const int h = r / per_head, k = r - h * per_head;
-        Where w;
-        w.xi = (t0 + t) * g.x_token + (int64_t)h * g.x_head;
-        w.oi = (t0 + t) * g.out_token + (int64_t)h * g.out_head;
-        if (k < rot) {
-            w.d = g.begin + (IL ? 2 * PER * k : PER * k);
-            w.dp = w.d + half;
-            w.pair = t * half + PER * k;
+    bool angles = false;
+    for (int kb = 0; kb < per_head; kb += kp) {              // (once, unless a head has more items than the block)
+        const int k = kb + k0;
+        const bool turn = k < rot, mine = k < per_head;
+        int d, second = 0;                                   // first element, its second vector
+        if (turn) {
+            d = g.begin + (IL ? 2 * PER * k : PER * k);
+            second = IL ? 1 : half;
         } else {
             const int c = (k - rot) * V;
-            w.d = c < g.begin ? c : c + g.dim;
-            w.dp = 0;
-            w.pair = -1;
+            d = c < g.begin ? c : c + g.dim;
         }
-        return w;
-    };
-    using VT = Vec<T, V>;
-    for (int base = 0; base < items; base += NT * UNROLL) {
-        VT a[UNROLL], b[UNROLL];
+        const T *xt = static_cast<const T *>(g.x) + h0 * g.x_head + d;
+        T *ot = static_cast<T *>(g.out) + h0 * g.out_head + d;
+        const int n = mine ? heads : 0;
+        VT a[U], b[TWO ? U : 1];
+        auto load = [&](int ti, int rd) {
+            const T *p = xt + ((t0 + ti) * g.x_token + rd * U * xs);
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int i = base + u * NT + (int)threadIdx.x;
-            if (i >= items) continue;
-            const Where w = where(i);
-            a[u] = *reinterpret_cast<const VT *>(x + w.xi + w.d);
-            if (w.pair >= 0) {
-                if (!IL) b[u] = *reinterpret_cast<const VT *>(x + w.xi + w.dp);
-                else if (V == 1) b[u] = *reinterpret_cast<const VT *>(x + w.xi + w.d + 1);
-            }
-        }
-        if (base == 0) {
-            for (int k = threadIdx.x; k < nt * half; k += NT) {
-                const int t = k / half;
-                double s, c;
-                sincos((double)__ldg(g.positions + t0 + t) * (double)__ldg(g.inv_freq + (k - t * half)), &s, &c);
-                if (g.transposed) s = -s;
-                cs[k] = make_float2((float)(c * g.scale), (float)(s * g.scale));
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int i = base + u * NT + (int)threadIdx.x;
-            if (i >= items) continue;
-            const Where w = where(i);
-            if (w.pair >= 0) {
-                if (IL && V > 1) {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        const float2 q = cs[w.pair + j];
-                        const float p0 = to_f(a[u].e[(2 * j) % V]), p1 = to_f(a[u].e[(2 * j + 1) % V]);
-                        a[u].e[(2 * j) % V] = from_f<T>(p0 * q.x - p1 * q.y);
-                        a[u].e[(2 * j + 1) % V] = from_f<T>(p1 * q.x + p0 * q.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        const float2 q = cs[w.pair + j];
-                        const float p0 = to_f(a[u].e[j]), p1 = to_f(b[u].e[j]);
-                        a[u].e[j] = from_f<T>(p0 * q.x - p1 * q.y);
-                        b[u].e[j] = from_f<T>(p1 * q.x + p0 * q.y);
-                    }
+            for (int u = 0; u < U; ++u) {
+                if ((rd * U + u) * step < n) {
+                    a[u] = *reinterpret_cast<const VT *>(p + u * xs);
+                    if (TWO && turn) b[TWO ? u : 0] = *reinterpret_cast<const VT *>(p + u * xs + second);
                 }
             }
-            *reinterpret_cast<VT *>(out + w.oi + w.d) = a[u];
-            if (w.pair >= 0) {
-                if (!IL) *reinterpret_cast<VT *>(out + w.oi + w.dp) = b[u];
-                else if (V == 1) *reinterpret_cast<VT *>(out + w.oi + w.d + 1) = b[u];
+        };
+        load(0, 0);
+        if (!angles) {
+            // the first loads are in flight: now the angles
+            for (int i = threadIdx.x; i < nt * half; i += threads) {
+                const int ti = i / half;
+                double sn, cn;
+                sincos((double)__ldg(g.positions + t0 + ti) * (double)__ldg(g.inv_freq + (i - ti * half)), &sn, &cn);
+                if (g.transposed) sn = -sn;
+                cs[i] = make_float2((float)(cn * g.scale), (float)(sn * g.scale));
+            }
+            __syncthreads();
+            angles = true;
+        }
+        for (int ti = 0; ti < nt; ++ti) {
+            float2 c[PER];
+            if (turn) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) c[j] = cs[ti * half + PER * k + j];
+            }
+            for (int rd = 0; rd < rounds; ++rd) {
+                T *o = ot + ((t0 + ti) * g.out_token + rd * U * os);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if ((rd * U + u) * step >= n) continue;
+                    if (turn) {
+#pragma unroll
+                        for (int j = 0; j < PER; ++j) {
+                            T &lo = IL && V > 1 ? a[u].e[(2 * j) % V] : a[u].e[j % V];
+                            T &hi = IL && V > 1 ? a[u].e[(2 * j + 1) % V] : b[TWO ? u : 0].e[j % V];
+                            const float p0 = to_f(lo), p1 = to_f(hi);
+                            lo = from_f<T>(p0 * c[j].x - p1 * c[j].y);
+                            hi = from_f<T>(p1 * c[j].x + p0 * c[j].y);
+                        }
+                    }
+                    store<T, V>(o + u * os, a[u]);
+                    if (TWO && turn) store<T, V>(o + u * os + second, b[TWO ? u : 0]);
+                }
+                // the next round's vectors (the next token's after the last)
+                const bool wrap = rd + 1 == rounds;
+                if (!wrap || ti + 1 < nt) load(wrap ? ti + 1 : ti, wrap ? 0 : rd + 1);
             }
         }
     }
