@@ -10,13 +10,19 @@
 // carry positions in every head's score; the factor 16 keeps a token whose RoPE dims are
 // larger than its normalised latent from coarsening the scale of the latent.
 //
-// A code is decided by which side of a border a value falls on, so everything up to the code
-// is evaluated in fp64 and rounded once: a value is taken to fp32 by rounding to odd, which
-// cannot move it onto or across a border of the 4-bit significands, and from there (power-of
-// -two scaling is exact) to e4m3.  fp32 all the way would misplace about one code in a
-// million.
-// HBM-bound at its floor (1.4 KB read and about 0.8 KB written per token).  One warp per
-// token; lane i owns RoPE pair i of both parts, so the angle it evaluates needs no exchange.
+// A code is decided by which side of a border a value falls on; the codes are those of an
+// evaluation in fp64.  The key and the RoPE dims (6 of a lane's 22 values) are evaluated in
+// fp64 and rounded once: a value is taken to fp32 by rounding to odd, which cannot move it
+// onto or across a border of the 4-bit significands, and from there (power-of-two scaling is
+// exact) to e4m3.  The 512 latent dims go in fp32 with a bound on their error (below); a token
+// with a value too near a border, or out of the bound's range, is evaluated again in fp64.
+// The border cases are 2 % of the tokens; fp64 for all cost 29.4 us at 32768 tokens, much of
+// it conversions between the formats, which run at 8 cycles a warp instruction.
+// One warp per token; lane i owns RoPE pair i of both parts, so the angle it evaluates needs
+// no exchange.  1.4 KB read and 0.8 KB written per token: 10.9 us at 32768 tokens and the copy
+// bandwidth; measured 21.6 us, bound by issue (about 500 instructions a token, of them the fp64
+// sine and cosine 1.5 us) and by what a token's chain of loads, sums and roots leaves uncovered.
+// 64 tokens: 3.1 us.
 #pragma once
 
 #include "cache_write.cuh"
@@ -65,10 +71,14 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
 
+constexpr uint32_t WINDOW = 12;       // ulp: the largest error of a latent value in fp32
+
+constexpr int FP8_WARPS = 4;          // (8: 24.4 us at 32768 tokens against 22.6)
+
 enum KeyForm { KEY_BF16 = 0, KEY_E4M3 = 1, KEY_UE8M0 = 2 };
 
 template <int FORM>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * FP8_WARPS, 8)
 cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __nv_bfloat16 *__restrict__ kv_raw,
                        const int32_t *__restrict__ pos, const int32_t *__restrict__ rows,
                        const float *__restrict__ ln_w, const float *__restrict__ ln_b,
@@ -76,30 +86,50 @@ cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __n
                        unsigned char *__restrict__ k_cache, void *__restrict__ k_scale,
                        unsigned char *__restrict__ kv_cache, unsigned char *__restrict__ kv_scale) {
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const int t = blockIdx.x * FP8_WARPS + (threadIdx.x >> 5);
     if (t >= n) return;                                       // whole warp
+    // ---- loads, all before the first use: indexer key dims lane + 32 j; latent dims 4 lane + 128 j
+    // and the 3 after; RoPE pair `lane`
     const int64_t row = __ldg(rows + t);
+    const int p = __ldg(pos + t);
+    uint16_t xr[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xr[j] = __ldg(reinterpret_cast<const uint16_t *>(k_raw) + (int64_t)t * 128 + lane + 32 * j);
+    const uint2 *src = reinterpret_cast<const uint2 *>(kv_raw + (int64_t)t * 576);
+    uint2 zw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) zw[j] = __ldg(src + lane + 32 * j);
+    const uint32_t zr = __ldg(reinterpret_cast<const uint32_t *>(src + 128) + lane);
+    double sn, cs;
+    sincos((double)p * (double)__ldg(inv_freq + lane), &sn, &cs);
     if (row < 0) return;                                      // a token without a row (padding)
-    // ---- loads: indexer key dims lane + 32 j; 16 latent dims; RoPE pair `lane`
     float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __bfloat162float(k_raw[(int64_t)t * 128 + lane + 32 * j]);
-    const uint4 *src = reinterpret_cast<const uint4 *>(kv_raw + (int64_t)t * 576) + 2 * lane;
-    const uint4 za = __ldg(src), zb = __ldg(src + 1);
-    const __nv_bfloat162 zr = reinterpret_cast<const __nv_bfloat162 *>(kv_raw + (int64_t)t * 576 + 512)[lane];
-    double sn, cs;
-    sincos((double)__ldg(pos + t) * (double)__ldg(inv_freq + lane), &sn, &cs);
+    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float((uint32_t)xr[j] << 16);
 
     // ---- indexer key
     {
-        const double mean = warp_sum_d(((double)x[0] + x[1]) + ((double)x[2] + x[3])) * (1.0 / 128.0);
-        double y[4], ss = 0.0;
+        // Sum x and sum x^2 in one reduction: lanes 0-15 end with the first, 16-31 with the second,
+        // then they swap.  The variance loses nothing by the difference: while the exponents of x lie
+        // within 15 binades both sums are exact (8-bit significands), and fma rounds once; beyond, some
+        // x is far from the largest, the variance is at least 2^-9 of the mean square, and the error 2^-41.
+        double y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = x[j] - mean;
-            ss = fma(y[j], y[j], ss);
-        }
-        const double inv = 1.0 / sqrt(warp_sum_d(ss) * (1.0 / 128.0) + (double)eps);
+        for (int j = 0; j < 4; ++j) y[j] = x[j];
+        const double s1 = (y[0] + y[1]) + (y[2] + y[3]);
+        const double s2 = fma(y[0], y[0], y[1] * y[1]) + fma(y[2], y[2], y[3] * y[3]);
+        const bool upper = lane >= 16;
+        double keep = (upper ? s2 : s1) + __shfl_xor_sync(0xffffffffu, upper ? s1 : s2, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+        const double other = __shfl_xor_sync(0xffffffffu, keep, 16);
+        const double sum = upper ? other : keep, sq = upper ? keep : other;
+        const double mean = sum * (1.0 / 128.0);
+        double var = fma(-sum, mean, sq) * (1.0 / 128.0);
+        var = var < 0.0 ? 0.0 : var;                          // (a NaN stays)
+        const double inv = rsqrt(var + (double)eps);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] -= mean;
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = fma(y[j] * inv, (double)__ldg(ln_w + lane + 32 * j), (double)__ldg(ln_b + lane + 32 * j));
         const double u = y[0], v = y[1];
@@ -111,27 +141,31 @@ cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __n
             for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = __float2bfloat16_rn(round_odd(y[j]));
         } else {
             float f[4];
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (FORM == KEY_UE8M0) f[j] = round_odd(y[j]);
-                else f[j] = (float)y[j];
-                m = max(m, abs_bits(f[j]));
-            }
-            m = warp_max_u(m);
             if (FORM == KEY_UE8M0) {
-                const uint32_t byte = scale_byte(m);
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[j] = round_odd(y[j]);
+                    m = max(m, abs_bits(f[j]));
+                }
+                const uint32_t byte = scale_byte(warp_max_u(m));
                 const float si = scale_inverse(byte);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j] *= si;
                 if (lane == 0) static_cast<unsigned char *>(k_scale)[row] = (unsigned char)byte;
             } else {
-                // fp32 scale amax / 448 (1 for a zero row): amax in fp64, the codes of y / scale in fp64
-                double am = fmax(fmax(fabs(y[0]), fabs(y[1])), fmax(fabs(y[2]), fabs(y[3])));
+                // fp32 scale amax / 448 (1 for a zero row), from amax in fp64: the largest upper word,
+                // then the largest lower word that goes with it; the codes of y / scale in fp64
+                uint32_t h = 0, l = 0;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) am = fmax(am, __shfl_xor_sync(0xffffffffu, am, o));
+                for (int j = 0; j < 4; ++j) h = max(h, (uint32_t)__double2hiint(y[j]) & 0x7fffffffu);
+                h = warp_max_u(h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    l = max(l, ((uint32_t)__double2hiint(y[j]) & 0x7fffffffu) == h ? (uint32_t)__double2loint(y[j]) : 0u);
+                const double am = __hiloint2double((int)h, (int)warp_max_u(l));
                 float sc = am > 0.0 ? (float)(am / 448.0) : 1.0f;
-                if (m >= 0x7f800000u) sc = __uint_as_float(0x7fc00000u);
+                if (abs_bits((float)am) >= 0x7f800000u) sc = __uint_as_float(0x7fc00000u);
                 const double si = 1.0 / (double)sc;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j] = round_odd(y[j] * si);
@@ -146,43 +180,75 @@ cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __n
         }
     }
 
-    // ---- latent: lane holds dims 16 lane .. 16 lane + 15 and RoPE pair `lane`
-    const uint32_t w8[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
-    float z[16];
-    double ss = 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&w8[j]);
-        z[2 * j] = __low2float(h);
-        z[2 * j + 1] = __high2float(h);
-        ss = fma((double)z[2 * j], (double)z[2 * j], ss);
-        ss = fma((double)z[2 * j + 1], (double)z[2 * j + 1], ss);
-    }
-    const double rinv = 1.0 / sqrt(warp_sum_d(ss) * (1.0 / 512.0) + (double)eps);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 wt = __ldg(reinterpret_cast<const float4 *>(rms_w + 16 * lane) + j);
-        const float w4[4] = {wt.x, wt.y, wt.z, wt.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            z[4 * j + e] = round_odd((double)z[4 * j + e] * rinv * (double)w4[e]);
-            m = max(m, abs_bits(z[4 * j + e]));
-        }
-    }
-    const double ru = __low2float(zr), rv = __high2float(zr);
+    // ---- latent.  A lane's 16 dims lie 128 apart in fours, so that each load of the weights covers
+    // whole lines: with 16 in a row the weights' loads alone were 64 of 73 L1 wavefronts a token.
+    const double ru = __uint_as_float(zr << 16), rv = __uint_as_float(zr & 0xffff0000u);
     // rot / 16: an exact scaling, so the maximum over both parts is one maximum
     const float r0 = round_odd(ru * cs - rv * sn) * (1.0f / KV8_ROPE_GAIN);
     const float r1 = round_odd(rv * cs + ru * sn) * (1.0f / KV8_ROPE_GAIN);
-    m = warp_max_u(max(m, max(abs_bits(r0), abs_bits(r1))));
+    const uint32_t mr = max(abs_bits(r0), abs_bits(r1));
+    const uint32_t w8[8] = {zw[0].x, zw[0].y, zw[1].x, zw[1].y, zw[2].x, zw[2].y, zw[3].x, zw[3].y};
+    float2 z[8];
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        z[j] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w8[j]));
+        acc[j & 1] = __ffma2_rn(z[j], z[j], acc[j & 1]);
+    }
+    // In units of 2^-24: the squares are exact, 3 sums here, 2 to one number, 5 over the warp, eps:
+    // 11, halved by the square root; rsqrtf 2 ulp = 4; the two products 2: 11.5, or as many ulp.
+    const float rinv = rsqrtf(warp_sum_f((acc[0].x + acc[1].x) + (acc[0].y + acc[1].y)) * (1.0f / 512.0f) + eps);
+    const float2 rinv2 = make_float2(rinv, rinv);
+    uint32_t near = 0xffffffffu;
+    float zm = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 wt = __ldg(reinterpret_cast<const float4 *>(rms_w) + lane + 32 * j);
+        z[2 * j] = __fmul2_rn(z[2 * j], __fmul2_rn(make_float2(wt.x, wt.y), rinv2));
+        z[2 * j + 1] = __fmul2_rn(z[2 * j + 1], __fmul2_rn(make_float2(wt.z, wt.w), rinv2));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // every border (of codes and of the scale) has at most 5 significant bits, 19 zeros below;
+        // so have infinities, and the NaN of a product, which fmaxf passes over, is 1 below that
+        zm = fmaxf(zm, fmaxf(fabsf(z[j].x), fabsf(z[j].y)));
+        near = min(near, min((__float_as_uint(z[j].x) + WINDOW) << 13, (__float_as_uint(z[j].y) + WINDOW) << 13));
+    }
+    uint32_t m = warp_max_u(max(mr, __float_as_uint(zm)));
+    // The bound holds for the values that reach a code other than 0 (2^-20 of the largest) if nothing
+    // on the way to them was below 2^-126: 2^-40 <= amax <= 2^100 and 2^-30 <= rinv <= 2^30 see to that.
+    const bool unsure = near < (2 * WINDOW) << 13 || m < 0x2b800000u || m > 0x71800000u ||
+                        !(rinv >= 0x1p-30f && rinv <= 0x1p30f);
+    if (__any_sync(0xffffffffu, unsure)) {
+        double ss = 0.0;
+#pragma unroll 2
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w8[j]));
+            ss = fma((double)v.x, (double)v.x, ss);
+            ss = fma((double)v.y, (double)v.y, ss);
+        }
+        const double rd = 1.0 / sqrt(warp_sum_d(ss) * (1.0 / 512.0) + (double)eps);
+        m = mr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w8[j]));
+            const float2 wt = __ldg(reinterpret_cast<const float2 *>(rms_w) + 2 * lane + 64 * (j >> 1) + (j & 1));
+            z[j].x = round_odd((double)v.x * rd * (double)wt.x);
+            z[j].y = round_odd((double)v.y * rd * (double)wt.y);
+            m = max(m, max(abs_bits(z[j].x), abs_bits(z[j].y)));
+        }
+        m = warp_max_u(m);
+    }
     const uint32_t byte = scale_byte(m);
     const float si = scale_inverse(byte);
-    uint32_t o[4];
+    const float2 si2 = make_float2(si, si);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = __fmul2_rn(z[j], si2);
+    unsigned char *dst = kv_cache + row * KV8_CODES;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        o[j] = e4m3x2(z[4 * j] * si, z[4 * j + 1] * si) | e4m3x2(z[4 * j + 2] * si, z[4 * j + 3] * si) << 16;
-    unsigned char *dst = kv_cache + row * KV8_CODES;
-    reinterpret_cast<uint4 *>(dst)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint32_t *>(dst)[lane + 32 * j] =
+            e4m3x2(z[2 * j].x, z[2 * j].y) | e4m3x2(z[2 * j + 1].x, z[2 * j + 1].y) << 16;
     const uint32_t hi = e4m3x2(r0 * si, r1 * si);
     // the remainders are exact in fp32 (r has 24 bits, hi the upper ones of them) except for the
     // odd-rounded last bit, far below a border of lo

@@ -723,9 +723,9 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
         if (q == nullptr || !aligned16(q)) return DSA_ERR_INVALID_ARG;
     if (kv_scale_cache == nullptr || (idx_dtype == DSA_BF16) != (k_scale_cache == nullptr)) return DSA_ERR_INVALID_ARG;
     if (idx_dtype == DSA_E4M3 && (reinterpret_cast<uintptr_t>(k_scale_cache) & 3u) != 0) return DSA_ERR_INVALID_ARG;
-    const unsigned grid = (unsigned)(((int64_t)n_tokens + dsa::cache::WARPS - 1) / dsa::cache::WARPS);
+    const unsigned grid = (unsigned)(((int64_t)n_tokens + dsa::cache::FP8_WARPS - 1) / dsa::cache::FP8_WARPS);
     auto launch = [&](auto kernel) {
-        kernel<<<grid, 32 * dsa::cache::WARPS, 0, (cudaStream_t)stream>>>(
+        kernel<<<grid, 32 * dsa::cache::FP8_WARPS, 0, (cudaStream_t)stream>>>(
             n_tokens, reinterpret_cast<const __nv_bfloat16 *>(k_idx_raw), reinterpret_cast<const __nv_bfloat16 *>(kv_raw),
             positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, eps, static_cast<unsigned char *>(k_idx_cache),
             k_scale_cache, static_cast<unsigned char *>(kv_cache), static_cast<unsigned char *>(kv_scale_cache));

@@ -355,6 +355,30 @@ def test_write_scales_of_unusual_rows(form):
     _check_write(i, 64, form)
 
 
+def test_write_values_on_and_next_to_code_borders():
+    """The latent dims are evaluated in fp32 where that decides the code: values that lie on a border
+    between two codes, or one unit in the last place beside it, must come out as in 64 bits."""
+    i = _write_inputs(8, 64, seed=8)
+    sign = torch.sign(torch.randn(8, 512, device=DEV))
+    i["kv_raw"][:, :512] = sign * 2.0 ** torch.arange(-3, 5, device=DEV)[:, None]   # |z| / rms is 1 exactly
+    i["kv_raw"][:, 512:] = 0
+    ties = ref.E4M3[:127]
+    ties = (ties[1:] + ties[:-1]) / 2                          # 126 borders, 2^-10 .. 432
+    w = np.concatenate([ties, np.nextafter(ties.astype(np.float32), np.float32(0)),
+                        np.nextafter(ties.astype(np.float32), np.float32(1e9)), ref.E4M3[:126], [1, 2, 3, 5, 7, 1, 1, 0]])
+    for top in (448.0, np.nextafter(np.float32(448), np.float32(1e9))):   # the scale's own border
+        w[-3:-1] = top, top
+        i["rms_w"] = torch.tensor(w[:512].astype(np.float32), device=DEV)
+        assert i["rms_w"].numel() == 512
+        _check_write(i, 64, "ue8m0", eps=0.0)
+    i["rms_w"] = i["rms_w"] * 2.0 ** -100                      # out of the range that fp32 decides
+    _check_write(i, 64, "ue8m0", eps=0.0)
+
+
+def test_write_many_tokens_have_the_codes_of_64_bits():
+    _check_write(_write_inputs(16400, 20000, seed=9), 20000, "e4m3")
+
+
 def test_write_rows_with_nan_or_infinity_get_a_nan_scale():
     i = _write_inputs(6, 64, seed=7)
     i["kv_raw"][0, 3] = float("nan")
