@@ -16,7 +16,7 @@
 // registers) and goes from head to head by adding strides: placing each vector by divisions
 // cost more instructions (177 a vector) than rotating it.
 // 8192 tokens x 128 heads x 64 dims out of [.., 192] rows into [.., 576] rows (268 MB, 41 us at
-// the copy bandwidth): 59 to 65 us; 5003 x 64 heads of 128 dims, all copied: 40 us (164 MB, 25 us).
+// the copy bandwidth): 57 us; 5003 x 64 heads of 128 dims, half of them copied: 39 us (164 MB, 25 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -69,11 +69,13 @@ __device__ __forceinline__ void store(T *p, const Vec<T, V> &v) {
 // rotated part.  Threads beyond a whole number of heads idle; the launch sizes the block by the
 // items of a token.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(NT, !IL && V > 1 ? 5 : 1) rope_kernel(Args g) {
+__global__ void __launch_bounds__(NT, V == 1 ? 1 : IL ? 4 : 5) rope_kernel(Args g) {
     constexpr int PER = IL ? (V == 1 ? 1 : V / 2) : V;       // pairs of a rotation item
     constexpr bool TWO = !IL || V == 1;                      // an item has a second vector
-    // heads in flight per thread (8192 x 128 interleaved: 62 us with 4, 65 with 2; 5003 x 64 half
-    // layout: 45 us with 1 and at most 51 registers, 50 with 1 and 62, 57 to 73 with 2)
+    // heads in flight per thread, and CTAs per SM (registers).  8192 x 128 heads, interleaved: 57 us
+    // with 4 heads and 4 CTAs, 64 with 3 CTAs, 59 with 2 heads and 5, 66 with 6, 69 with 1 and 7 (59
+    // as a copy without the rotation, with 3 CTAs).  5003 x 64 heads, half layout: 39 us with 1 head
+    // and 5 CTAs, 42 with 6; before the streamed stores 45 against 50 with 4 CTAs, 57 to 73 with 2 heads.
     constexpr int U = V == 1 ? 2 : IL ? 4 : 1;
     using VT = Vec<T, V>;
     __shared__ __align__(16) float2 cs[MAX_PAIRS];
