@@ -775,9 +775,17 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *po
     if (r->x_token_stride < 0 || r->x_head_stride < 0 || r->out_token_stride < 0 || r->out_head_stride < 0)
         return DSA_ERR_INVALID_ARG;
     if (!isfinite(r->scale)) return DSA_ERR_INVALID_ARG;
-    // output rows must be distinct: every dimension longer than 1 moves by at least a head
+    // output rows must be distinct: every dimension longer than 1 moves by at least a head, and the
+    // wider of the two strides by at least what the other dimension spans
     if ((r->n_tokens > 1 && r->out_token_stride < r->head_dim) || (r->n_heads > 1 && r->out_head_stride < r->head_dim))
         return DSA_ERR_INVALID_ARG;
+    if (r->n_tokens > 1 && r->n_heads > 1) {
+        const bool by_token = r->out_token_stride >= r->out_head_stride;
+        const int64_t wide = by_token ? r->out_token_stride : r->out_head_stride;
+        const int64_t narrow = by_token ? r->out_head_stride : r->out_token_stride;
+        const int64_t count = by_token ? r->n_heads : r->n_tokens;
+        if ((wide - r->head_dim) / narrow < count - 1) return DSA_ERR_INVALID_ARG;
+    }
     if (r->n_tokens == 0 || r->n_heads == 0) return DSA_OK;
     const uintptr_t esize = r->dtype == DSA_ROPE_FP32 ? 4 : 2;
     if (!x || !positions || !inv_freq || !out) return DSA_ERR_INVALID_ARG;
@@ -803,8 +811,8 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *po
                                  : r->rope_dim / 2 + (in_place ? 0 : r->head_dim - r->rope_dim);
     const int64_t per_token = per_head * r->n_heads;
     // tokens per CTA: about four items per thread, or up to eight tokens where that still leaves a
-    // full grid (8192 tokens x 128 heads x 64 dims: 89 us with one, 76 with two, 73 with four or eight, in an earlier form); no more
-    // than the angle table holds
+    // full grid (8192 tokens x 128 heads x 64 dims, in an earlier form: 89 us with one, 76 with two,
+    // 73 with four or eight); no more than the angle table holds
     int64_t nt = 4 * dsa::rope::NT / per_token;
     int64_t full = r->n_tokens / dsa::rope::FULL_GRID;
     full = full < 8 ? full : 8;

@@ -78,31 +78,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_for(bar, parity, WAIT_LIMIT_NS);
 }
 
-// The same wait for warps that have long waits beside busy ones: each try suspends the warp
-// for up to 1 ms instead of the default few cycles, so that it takes no issue slots.
-__device__ __forceinline__ bool mbar_try_wait_suspended(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(1000000u)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait_suspended(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
-        if (mbar_try_wait_suspended(bar, parity)) return true;
-        if (globaltimer() - t0 > WAIT_LIMIT_NS) {
-            raise_error(ERR_WAIT_TIMEOUT);
-            return false;
-        }
-    }
-}
-
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {

@@ -344,7 +344,8 @@ typedef struct dsa_rope_desc {
  * from the gradient of out on the rotated dims (copied dims pass through).
  *   positions : [n_tokens] int32      inv_freq : [rope_dim / 2] fp32
  * Pointers need the alignment of their element type only (16-byte aligned slices and
- * strides are faster); strides >= 0; |scale| finite.
+ * strides are faster); |scale| finite.  Strides >= 0: those of x may be 0 (a broadcast input),
+ * those of out keep its heads apart, in [tokens, heads] or [heads, tokens] order.
  */
 dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *positions,
                       const float *inv_freq, void *out, dsa_stream_t stream);
@@ -381,8 +382,8 @@ dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, 
  *     kv_cache[row, 512:576] = hi = Q(rot / (16 s)),  kv_cache[row, 576:640] = Q(rot / (16 s) - hi)
  *   so the row stands for the latent code * s and the RoPE dims (hi + lo) * 16 s.  Every
  *   element keeps 4 significant bits (RoPE dims: 8) down to 2^-15 of the largest one.
- * Power-of-two scales are at least 2^-126.  Arithmetic up to the code in fp64: each code is
- * the nearest one to the exact value.  A row that holds an infinity or a NaN gets the scale
+ * Power-of-two scales are at least 2^-126.  Each code is the nearest one to the value of a
+ * 64-bit evaluation.  A row that holds an infinity or a NaN gets the scale
  * NaN (0xFF) and NaN codes.  Tokens with rows[t] < 0 are passed over; other rows are left as
  * they were.
  *   kv_cache : uint8 [.., 640]   kv_scale_cache : uint8 [..]     other tensors as dsa_cache_write
@@ -402,7 +403,8 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * rows without a valid slot.  What a masked slot's cache row holds (NaN included) has no
  * effect.
  * Accuracy: q and the probabilities enter the tensor cores as two e4m3 numbers each (8
- * significant bits), products are exact and sums are fp32.  A probability is held relative to
+ * significant bits; for q no finer than 2^-17 of its head's largest element, the RoPE dims
+ * counted 16 times), products are exact and sums are fp32.  A probability is held relative to
  * the largest scale among the keys its row has read so far: next to keys whose scale is 2^n
  * times its own, a key keeps 2^-14 of the largest probability's weight times 2^n.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd

@@ -835,3 +835,56 @@ def test_serving_steps_together(form):
         cached += n
         head += counts[1:2]
     dsa.dsa_check_device_errors()
+
+
+def test_serving_step_captured_and_replayed():
+    """A step's calls in one graph, replayed with other lengths and inputs, give what the calls give eagerly."""
+    B, T, n_pages, topk = 3, 40, 24, 64
+    g = torch.Generator(device=DEV).manual_seed(31)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    weights = [torch.ones(128, device=DEV), torch.zeros(128, device=DEV), torch.ones(512, device=DEV)]
+    freq = dsa.dsa_rope_frequencies(64)[0].to(DEV)
+    free = torch.randperm(n_pages, generator=g, device=DEV).to(I32)
+    idx = torch.arange(topk, dtype=I32, device=DEV).expand(T, topk).contiguous()
+
+    def state():
+        z = lambda *s, dtype=I32: torch.zeros(*s, dtype=dtype, device=DEV)  # noqa: E731
+        s = dict(cached=z(B), new=z(B), table=torch.full((B, 8), -1, dtype=I32, device=DEV), head=z(1), cu_q=z(B + 1),
+                 cu_k=z(B + 1), pos=z(T), rows=z(T), counts=z(4), k_raw=z(T, 128, dtype=torch.bfloat16),
+                 kv_raw=z(T, 576, dtype=torch.bfloat16), x=z(T, 128, 192, dtype=torch.bfloat16),
+                 q=z(T, 128, 576, dtype=torch.bfloat16), out=z(T, 128, 512, dtype=torch.bfloat16), lse=z(T, 128, dtype=torch.float32),
+                 caches=_caches(n_pages * 64, "ue8m0"))
+        s["p"] = dsa.make_problem(B, T, n_pages * 64, T, 512, topk, cu_q=s["cu_q"], cu_k=s["cu_k"], block_table=s["table"])
+        s["ws"] = z(dsa.dsa_sparse_mla_fp8_workspace_size(s["p"]), dtype=torch.uint8)
+        return s
+
+    def step(s):
+        dsa.dsa_paged_plan(s["cached"], s["new"], s["table"], free, s["cu_q"], s["cu_k"], s["pos"], s["rows"], s["counts"],
+                           n_pages=n_pages, free_head=s["head"])
+        dsa.dsa_cache_write_fp8(s["k_raw"], s["kv_raw"], s["pos"], s["rows"], *weights, freq, *s["caches"])
+        dsa.dsa_rope(s["x"][..., 128:], s["pos"], freq, s["q"][..., 512:])
+        dsa.dsa_sparse_mla_fp8_fwd(s["p"], s["q"], s["caches"][2], s["caches"][3], idx, s["out"], s["lse"], s["ws"])
+
+    eager, captured = state(), state()
+    step(captured)                                          # an empty batch: no lengths yet
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(captured)
+    for new in ([20, 0, 13], [1, 17, 1], [1, 1, 38], [0, 0, 0]):
+        drawn = dict(new=torch.tensor(new, dtype=I32, device=DEV), k_raw=r(T, 128), kv_raw=r(T, 576), x=r(T, 128, 192))
+        q = r(T, 128, 512).to(torch.bfloat16)
+        for s in (eager, captured):
+            for k, v in drawn.items():
+                s[k].copy_(v)
+            s["q"][..., :512] = q
+        step(eager)
+        graph.replay()
+        for k in ("table", "cu_q", "cu_k", "pos", "rows", "counts", "q", "out", "lse"):
+            assert torch.equal(eager[k], captured[k]), k
+        assert all(torch.equal(a, b) for a, b in zip(eager["caches"], captured["caches"]))
+        live = sum(new)
+        assert torch.all(torch.isneginf(eager["lse"][live:])) and torch.all(torch.isfinite(eager["lse"][:live]))
+        for s in (eager, captured):
+            s["cached"] += s["new"]
+            s["head"] += s["counts"][1:2]
+    dsa.dsa_check_device_errors()

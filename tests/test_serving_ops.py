@@ -61,7 +61,9 @@ def _rope(x=FAKE, pos=FAKE, freq=FAKE, out=FAKE + (1 << 16), **kw):
 @pytest.mark.parametrize("kw", [dict(n_tokens=-1), dict(n_heads=-1), dict(head_dim=0), dict(rope_begin=-2),
                                 dict(rope_dim=0), dict(rope_dim=63), dict(rope_begin=2), dict(layout=2),
                                 dict(x_token_stride=-1), dict(out_head_stride=-1), dict(out_head_stride=63),
-                                dict(out_token_stride=0), dict(scale=math.inf), dict(scale=math.nan), dict(x=None),
+                                dict(out_token_stride=0), dict(out_token_stride=64), dict(out_token_stride=127),
+                                dict(out_token_stride=64, out_head_stride=192), dict(scale=math.inf),
+                                dict(scale=math.nan), dict(x=None),
                                 dict(pos=None), dict(freq=None), dict(out=None), dict(x=FAKE + 1), dict(freq=FAKE + 2),
                                 dict(dtype=2, out=FAKE + 2), dict(out=FAKE, x_head_stride=128)])
 def test_rope_refuses(kw):
