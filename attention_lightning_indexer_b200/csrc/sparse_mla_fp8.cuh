@@ -4,11 +4,17 @@
 //   z[t,h,i] = sm_scale * q[t,h,:] . kv[idx[t,i], :]     out = softmax(z) . kv[:, 0:512]
 //
 // Eight bits on the tensor cores without losing the other operand's: a bf16 number has 8
-// significant bits and e4m3 has 4, so q (and a probability) is the sum of two e4m3 numbers,
+// significant bits and e4m3 has 4, so q (and a probability) is the sum of two 8-bit numbers,
 // hi = Q(x) and lo = Q(x - hi), and every product with a cached code is two kind::f8f6f4
 // MMAs, each at twice the bf16 rate: the tensor time of the bf16 form, but the cached rows go
 // from HBM into the MMA as they are.  Nothing is dequantised, the gathers move 144 KB per CTA and
 // block instead of 272 KB, and a ring slot holds 128 dims of a key instead of 64.
+//
+// q's lo is e5m2: x - hi is at most 8 units of x's last bit, so its 3 significant bits are enough
+// (1 .. 8 are all among them), and its range reaches 2^-16: q is exact down to 2^-6 of a range
+// that ends at 448, where an e4m3 lo was off by 2^-10 below 2^-2 (lse off by 1e-4 at the worst,
+// since 16 times the RoPE dims sets the range; 9e-6 now).  A probability has more than 8 bits; its
+// lo is e4m3 (2^-9 of the value; e5m2 with TAU = 7.8, BASE = 1 below: 2^-8, and 2 % faster).
 //
 // The row's scale 2^e leaves the sums: S^T[key, h] is over codes, and its thread (which owns
 // one key) multiplies by 2^e; for the values, the probability takes the scale with it, P' =
@@ -133,12 +139,13 @@ __device__ __forceinline__ float warp_fmax(float v) {
     return r;
 }
 
-// Two fp16 numbers as hi = Q(x) and lo = Q(x - hi) (two e4m3 codes each).
+// Two fp16 numbers as hi = Q(x), e4m3, and lo = Q(x - hi), e4m3 or e5m2 (two codes each).
+template <__nv_fp8_interpretation_t LO>
 __device__ __forceinline__ void split_e4m3(__half2 x, uint32_t &hi, uint32_t &lo) {
     const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
     const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
     hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, LO);
 }
 
 struct Unit {
@@ -397,6 +404,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // The whole warp runs the loop and one elected lane issues, so that descriptors stay in
         // uniform registers; a lane of its own spent as long on issuing an MMA as it takes to run.
         const uint32_t idesc_qk = idesc_e4m3(256, 128);
+        const uint32_t idesc_qk_lo = idesc_qk | (1u << 10);                         // B e5m2
         const uint32_t idesc_pv = idesc_e4m3(256, 128) | (1u << 15) | (1u << 16);   // A and B MN-major
         // descriptors step by bytes / 16 in their low word
         const uint64_t dq = desc_sw128(q_s), da_k = desc_sw128(ring_s), da_mn = desc_sw128_mn(ring_s, C::ATOM);
@@ -441,7 +449,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             for (int kk = 0; kk < 4; ++kk) {
                                 const int qo = 2 * (a == ROPE ? (kk & 1) : kk);
                                 mma_f8_pair(d, da + 2 * kk, qh + qo, idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
-                                mma_f8_pair(d, da + 2 * kk, ql + qo, idesc_qk, 1u);
+                                mma_f8_pair(d, da + 2 * kk, ql + qo, idesc_qk_lo, 1u);
                             }
                             mma_commit_pair_both(empty(slot));
                         }
@@ -654,7 +662,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     for (int i = 0; i < 4; ++i) {
                         const float v0 = __uint_as_float(w[i] << 16), v1 = __uint_as_float(w[i] & 0xffff0000u);
                         // fp16 holds the 8 significant bits of bf16 down to 2^-24
-                        split_e4m3(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
+                        split_e4m3<__NV_E5M2>(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
                     }
                     const uint2 h = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
                     const uint2 l = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
@@ -895,7 +903,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             const uint64_t p2 = pack_f32x2(p0, p1);
                             l[8 * v + i] = add_f32x2(l[8 * v + i], p2);
                             unpack_f32x2(mul_f32x2(p2, kf2), p0, p1);
-                            split_e4m3(__floats2half2_rn(p0, p1), hi[i], lo[i]);
+                            split_e4m3<__NV_E4M3>(__floats2half2_rn(p0, p1), hi[i], lo[i]);
                         }
                         uint32_t h[4], g[4];
 #pragma unroll

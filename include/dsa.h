@@ -402,9 +402,9 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * slot (out = 0, lse = -inf).  Query rows behind the last sequence (t >= cu_q[B]) count as
  * rows without a valid slot.  What a masked slot's cache row holds (NaN included) has no
  * effect.
- * Accuracy: q and the probabilities enter the tensor cores as two e4m3 numbers each (8
- * significant bits; for q no finer than 2^-17 of its head's largest element, the RoPE dims
- * counted 16 times), products are exact and sums are fp32.  A probability is held relative to
+ * Accuracy: q and the probabilities enter the tensor cores as two 8-bit floats each.  q's
+ * elements are exact down to 2^-13 of their head's largest (the RoPE dims counted 16 times) and
+ * off by at most 2^-21 of it below; a probability keeps 8 significant bits.  Products are exact and sums are fp32.  A probability is held relative to
  * the largest scale among the keys its row has read so far: next to keys whose scale is 2^n
  * times its own, a key keeps 2^-14 of the largest probability's weight times 2^n.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd

@@ -133,13 +133,14 @@ def attention(q, key_rows, values, scale_bytes, sm_scale):
     l = p.sum(1, keepdims=True)
     out = p @ kv[:, :512] / l
     # Bounds.
-    # (1) q as two e4m3 numbers at scale 2^f, the smallest with max(|q_lat|, 16 |q_rope|) <= 448 * 2^f:
-    #     exact for elements of at least 2^-2 * 2^f (8 significant bits), else off by at most half
-    #     the smallest step, 2^-10 * 2^f (for 16 * q_rope: 2^-14 * 2^f on q_rope).
+    # (1) q as hi (e4m3) + lo (e5m2) at scale 2^f, the smallest with max(|q_lat|, 16 |q_rope|) <= 448 * 2^f:
+    #     from 2^-6 * 2^f on hi has 4 significant bits and the rest is at most 8 units of the 8th bit,
+    #     which e5m2's 3 bits hold; below, hi steps by 2^-9, the rest is at most 2^-10 and half its step
+    #     in e5m2 at most 2^-14 (times 2^f; for 16 * q_rope: 2^-18 on q_rope).
     top = np.maximum(np.abs(q[:, :512]).max(1), 16 * np.abs(q[:, 512:]).max(1))
     f = 2.0 ** scale_exponent(top)[:, None]
-    dq = np.concatenate([np.where(np.abs(q[:, :512]) < 0.25 * f, 2.0 ** -10 * f, 0),
-                         np.where(np.abs(16 * q[:, 512:]) < 0.25 * f, 2.0 ** -14 * f, 0)], 1)
+    dq = np.concatenate([np.where(np.abs(q[:, :512]) < 2.0 ** -6 * f, 2.0 ** -14 * f, 0),
+                         np.where(np.abs(16 * q[:, 512:]) < 2.0 ** -6 * f, 2.0 ** -18 * f, 0)], 1)
     # (2) 1280 products summed in fp32, added up 32 at a time: 40 additions at 2^-23 of the sum
     #     of magnitudes; the scaling and the exponent's argument add a few more.
     dz = sm_scale * (dq @ np.abs(kv).T + 48 * 2.0 ** -23 * (np.abs(q) @ np.abs(kv).T)) + 2.0 ** -22 * (np.abs(z) + np.abs(m))
