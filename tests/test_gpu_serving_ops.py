@@ -845,7 +845,6 @@ def test_serving_step_captured_and_replayed():
     weights = [torch.ones(128, device=DEV), torch.zeros(128, device=DEV), torch.ones(512, device=DEV)]
     freq = dsa.dsa_rope_frequencies(64)[0].to(DEV)
     free = torch.randperm(n_pages, generator=g, device=DEV).to(I32)
-    idx = torch.arange(topk, dtype=I32, device=DEV).expand(T, topk).contiguous()
 
     def state():
         z = lambda *s, dtype=I32: torch.zeros(*s, dtype=dtype, device=DEV)  # noqa: E731
@@ -853,17 +852,22 @@ def test_serving_step_captured_and_replayed():
                  cu_k=z(B + 1), pos=z(T), rows=z(T), counts=z(4), k_raw=z(T, 128, dtype=torch.bfloat16),
                  kv_raw=z(T, 576, dtype=torch.bfloat16), x=z(T, 128, 192, dtype=torch.bfloat16),
                  q=z(T, 128, 576, dtype=torch.bfloat16), out=z(T, 128, 512, dtype=torch.bfloat16), lse=z(T, 128, dtype=torch.float32),
-                 caches=_caches(n_pages * 64, "ue8m0"))
-        s["p"] = dsa.make_problem(B, T, n_pages * 64, T, 512, topk, cu_q=s["cu_q"], cu_k=s["cu_k"], block_table=s["table"])
+                 q_idx=z(T, 64, 128, dtype=torch.bfloat16), rotated=z(T, 64, 128, dtype=torch.bfloat16), w=z(T, 64, dtype=torch.float32),
+                 scores=z(T, dsa.scores_ld(512), dtype=torch.float32), idx=z(T, topk), caches=_caches(n_pages * 64, "bf16"))
+        s["p"] = dsa.make_problem(B, T, n_pages * 64, T, 512, topk, cu_q=s["cu_q"], cu_k=s["cu_k"], block_table=s["table"],
+                                  idx_dtype=dsa.DSA_BF16)
         s["ws"] = z(dsa.dsa_sparse_mla_fp8_workspace_size(s["p"]), dtype=torch.uint8)
         return s
 
     def step(s):
         dsa.dsa_paged_plan(s["cached"], s["new"], s["table"], free, s["cu_q"], s["cu_k"], s["pos"], s["rows"], s["counts"],
                            n_pages=n_pages, free_head=s["head"])
-        dsa.dsa_cache_write_fp8(s["k_raw"], s["kv_raw"], s["pos"], s["rows"], *weights, freq, *s["caches"])
+        dsa.dsa_cache_write_fp8(s["k_raw"], s["kv_raw"], s["pos"], s["rows"], *weights, freq, *s["caches"], idx_dtype=dsa.DSA_BF16)
         dsa.dsa_rope(s["x"][..., 128:], s["pos"], freq, s["q"][..., 512:])
-        dsa.dsa_sparse_mla_fp8_fwd(s["p"], s["q"], s["caches"][2], s["caches"][3], idx, s["out"], s["lse"], s["ws"])
+        dsa.dsa_rope(s["q_idx"], s["pos"], freq, s["rotated"], layout=dsa.DSA_ROPE_HALF, rope_dim=64)
+        dsa.dsa_indexer_scores(s["p"], s["rotated"], s["caches"][0], s["w"], s["scores"])
+        dsa.dsa_topk(s["p"], s["scores"], s["idx"])
+        dsa.dsa_sparse_mla_fp8_fwd(s["p"], s["q"], s["caches"][2], s["caches"][3], s["idx"], s["out"], s["lse"], s["ws"])
 
     eager, captured = state(), state()
     step(captured)                                          # an empty batch: no lengths yet
@@ -871,7 +875,8 @@ def test_serving_step_captured_and_replayed():
     with torch.cuda.graph(graph):
         step(captured)
     for new in ([20, 0, 13], [1, 17, 1], [1, 1, 38], [0, 0, 0]):
-        drawn = dict(new=torch.tensor(new, dtype=I32, device=DEV), k_raw=r(T, 128), kv_raw=r(T, 576), x=r(T, 128, 192))
+        drawn = dict(new=torch.tensor(new, dtype=I32, device=DEV), k_raw=r(T, 128), kv_raw=r(T, 576), x=r(T, 128, 192),
+                     q_idx=r(T, 64, 128), w=r(T, 64))
         q = r(T, 128, 512).to(torch.bfloat16)
         for s in (eager, captured):
             for k, v in drawn.items():
@@ -881,8 +886,9 @@ def test_serving_step_captured_and_replayed():
         graph.replay()
         for k in ("table", "cu_q", "cu_k", "pos", "rows", "counts", "q", "out", "lse"):
             assert torch.equal(eager[k], captured[k]), k
-        assert all(torch.equal(a, b) for a, b in zip(eager["caches"], captured["caches"]))
+        assert all(torch.equal(eager["caches"][i], captured["caches"][i]) for i in (0, 2, 3))
         live = sum(new)
+        assert torch.equal(eager["idx"][:live], captured["idx"][:live])
         assert torch.all(torch.isneginf(eager["lse"][live:])) and torch.all(torch.isfinite(eager["lse"][:live]))
         for s in (eager, captured):
             s["cached"] += s["new"]
