@@ -810,19 +810,25 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *po
     const int64_t per_head = vec ? (il ? r->rope_dim : r->rope_dim / 2) / v + (in_place ? 0 : (r->head_dim - r->rope_dim) / v)
                                  : r->rope_dim / 2 + (in_place ? 0 : r->head_dim - r->rope_dim);
     const int64_t per_token = per_head * r->n_heads;
-    // tokens per CTA: about four items per thread, or up to eight tokens where that still leaves a
-    // full grid (8192 tokens x 128 heads x 64 dims, in an earlier form: 89 us with one, 76 with two,
-    // 73 with four or eight); no more than the angle table holds
+    // tokens per CTA: about four items per thread, or two tokens where that still leaves a full grid
+    // (8192 tokens x 128 heads x 64 dims: 53 us with one or two, 55 with four, 57 with eight); no
+    // more than the angle table holds
     int64_t nt = 4 * dsa::rope::NT / per_token;
     int64_t full = r->n_tokens / dsa::rope::FULL_GRID;
-    full = full < 8 ? full : 8;
+    full = full < 2 ? full : 2;
     nt = nt > full ? nt : full;
     const int64_t fit = dsa::rope::MAX_PAIRS / (r->rope_dim / 2);
     nt = nt < fit ? nt : fit;
     nt = nt < dsa::rope::MAX_TOKENS ? nt : dsa::rope::MAX_TOKENS;
     a.tokens_per_cta = nt > 1 ? (int)nt : 1;
     const unsigned grid = (unsigned)(((int64_t)r->n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta);
-    const unsigned block = (unsigned)(per_token < dsa::rope::NT ? (per_token + 31) / 32 * 32 : dsa::rope::NT);
+    // threads: as many heads side by side as give every round the same number (64 heads of 12 items:
+    // four rounds of 16 heads in 192 threads, 35 us against 38 with 21, 21, 21 and 1 in 256)
+    const int64_t u = dsa::rope::heads_in_flight(vec, il);
+    const int64_t kp = per_head < dsa::rope::NT ? per_head : dsa::rope::NT, most = u * (dsa::rope::NT / kp);
+    const int64_t rounds = (r->n_heads + most - 1) / most;
+    const int64_t side = (r->n_heads + u * rounds - 1) / (u * rounds);
+    const unsigned block = (unsigned)((side * kp + 31) / 32 * 32);
     auto launch = [&](auto kernel) { kernel<<<grid, block, 0, (cudaStream_t)stream>>>(a); };
     if (r->dtype == DSA_ROPE_FP32) {
         if (vec) il ? launch(dsa::rope::rope_kernel<float, 4, true>) : launch(dsa::rope::rope_kernel<float, 4, false>);

@@ -16,7 +16,7 @@
 // registers) and goes from head to head by adding strides: placing each vector by divisions
 // cost more instructions (177 a vector) than rotating it.
 // 8192 tokens x 128 heads x 64 dims out of [.., 192] rows into [.., 576] rows (268 MB, 41 us at
-// the copy bandwidth): 57 us; 5003 x 64 heads of 128 dims, half of them copied: 39 us (164 MB, 25 us).
+// the copy bandwidth): 53 us; 5003 x 64 heads of 128 dims, half of them copied: 35 us (164 MB, 25 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -30,6 +30,13 @@ constexpr int NT = 256;
 constexpr int MAX_PAIRS = 512;       // (cos, sin) pairs kept per CTA
 constexpr int MAX_TOKENS = 16;       // tokens per CTA
 constexpr int FULL_GRID = 148 * 8;   // CTAs that keep every SM busy
+
+// Heads a thread has in flight (kernel and launch).  8192 x 128 heads, interleaved: 57 us with 4
+// and 4 CTAs per SM, 64 with 3 CTAs, 59 with 2 heads and 5, 66 with 6, 69 with 1 and 7 (59 as a
+// copy without the rotation, with 3 CTAs; all with eight tokens per CTA).  5003 x 64 heads, half
+// layout: 39 us with 1 head and 5 CTAs, 42 with 6; before the streamed stores 45 against 50 with
+// 4 CTAs, 57 to 73 with 2 heads.
+__host__ __device__ constexpr int heads_in_flight(bool vec, bool interleaved) { return !vec ? 2 : interleaved ? 4 : 1; }
 
 struct Args {
     const void *x;
@@ -66,17 +73,12 @@ __device__ __forceinline__ void store(T *p, const Vec<T, V> &v) {
 
 // A work item of a head is a rotation (V pairs in the half layout, V / 2 pairs of one vector
 // in the interleaved one, one pair where V = 1) or the copy of V elements outside the
-// rotated part.  Threads beyond a whole number of heads idle; the launch sizes the block by the
-// items of a token.
+// rotated part.  Threads beyond a whole number of heads idle.
 template <typename T, int V, bool IL>
 __global__ void __launch_bounds__(NT, V == 1 ? 1 : IL ? 4 : 5) rope_kernel(Args g) {
     constexpr int PER = IL ? (V == 1 ? 1 : V / 2) : V;       // pairs of a rotation item
     constexpr bool TWO = !IL || V == 1;                      // an item has a second vector
-    // heads in flight per thread, and CTAs per SM (registers).  8192 x 128 heads, interleaved: 57 us
-    // with 4 heads and 4 CTAs, 64 with 3 CTAs, 59 with 2 heads and 5, 66 with 6, 69 with 1 and 7 (59
-    // as a copy without the rotation, with 3 CTAs).  5003 x 64 heads, half layout: 39 us with 1 head
-    // and 5 CTAs, 42 with 6; before the streamed stores 45 against 50 with 4 CTAs, 57 to 73 with 2 heads.
-    constexpr int U = V == 1 ? 2 : IL ? 4 : 1;
+    constexpr int U = heads_in_flight(V > 1, IL);
     using VT = Vec<T, V>;
     __shared__ __align__(16) float2 cs[MAX_PAIRS];
     const int threads = (int)blockDim.x;
