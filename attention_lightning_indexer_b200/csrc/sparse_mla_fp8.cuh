@@ -27,7 +27,8 @@
 // the DSMEM traffic: the half of P'^T that belongs to the other CTA's heads goes there by
 // st.async, which counts its bytes on that CTA's barrier p_in (the odd CTA's warp 7 relays it
 // to the MMA thread), and the other arrivals carry nothing but the order of the tcgen05 and
-// proxy fences before them.
+// proxy fences before them.  Waits for what the other CTA sent acquire at cluster scope, which
+// costs nothing measurable.
 //
 // The schedule is that of the bf16 kernel (sparse_mla_pair.cuh): persistent CTA pairs take
 // (token, split) units in turn; blocks of 256 index slots, CTA c owns slots 128 c .. + 127 of
@@ -400,7 +401,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (ok) mbar_arrive(unit_free(j & 1));
             for (int b = 0; ok && b < nblocks; ++b, ++gb) {
                 mbar_expect_tx(p_in, 128 * 128);
-                ok = mbar_wait(p_in, gb & 1) && !misc[1];
+                ok = mbar_wait_cluster(p_in, gb & 1) && !misc[1];
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive_remote(p_full_lead);
             }
@@ -486,7 +487,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     if (elect_one()) mbar_expect_tx(p_in, 128 * 128);
                     // the previous unit's O^T has been read out
                     if (b == 0 && nq > 0) okw = okw && mbar_wait(o_free, (nq - 1) & 1);
-                    okw = okw && mbar_wait(p_full, gb & 1) && mbar_wait(p_in, gb & 1);
+                    okw = okw && mbar_wait_cluster(p_full, gb & 1) && mbar_wait_cluster(p_in, gb & 1);
                     fence_proxy_async_smem();
                     tc_fence_after();
 #pragma unroll
@@ -779,7 +780,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const int gb = gb0 + b;
                 const int sl = gb & (C::NINFO - 1);
                 const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
-                                  (b == 0 && !mbar_wait(qs_full(qslot), qphase)) ||
+                                  (b == 0 && !mbar_wait_cluster(qs_full(qslot), qphase)) ||
                                   !mbar_wait(s_full(gb & 1), (gb >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
@@ -827,7 +828,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float q = qs[h];
                     if (b == 0) mq[mqh + 2] = q;
                     const float m_old = -mq[mqh];
-                    const bool okx = mbar_wait(xbar(gb & 1), (gb >> 1) & 1);
+                    const bool okx = mbar_wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
                     const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * q;
                     const bool need = m_blk > m_old + C::TAU;
                     fs[h] = (need && m_old != -INFINITY) ? ex2_approx(m_old - m_blk) : 1.0f;
@@ -958,7 +959,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     st_async_f32(mapa_shared(sbase + C::OFF_XL + 4u * h, (uint32_t)peer), l_cta,
                                  mapa_shared(lbar, (uint32_t)peer));
                     if (st == 0) mbar_expect_tx(lbar, 128 * 4);
-                    const bool okl = mbar_wait(lbar, nq & 1);
+                    const bool okl = mbar_wait_cluster(lbar, nq & 1);
                     // the two CTAs add the same two numbers in the same order
                     const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
                     // O^T holds sum p 2^(e - er + BASE) code
