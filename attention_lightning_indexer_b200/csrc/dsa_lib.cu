@@ -339,6 +339,15 @@ dsa_status_t mla_launch(const dsa_problem_t *p, const void *q, const void *kv, c
                                                                                    sp.lse_part, ob, lse);
     return launch_status();
 }
+// Bytes of the split q of the units that wait for their turn: one image per CTA, as soon as there
+// are several units (a pair may take more than one where fewer SMs are free).
+size_t mla_fp8_image_bytes(const dsa_problem_t *p) {
+    int ns, bps;
+    mla_split_plan(p, &ns, &bps);
+    const int64_t units = (int64_t)p->total_q * ns;
+    if (units < 2) return 0;
+    return (size_t)(units < MLA_PAIRS ? units : MLA_PAIRS) * 2 * dsa::mla8::Cfg::QIMG;
+}
 // The attention over the 8-bit cache; split_ws holds the parts of split rows (mla_split_plan).
 dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *kv, const void *kv_scale, const int32_t *idx,
                             void *out, float *lse, cudaStream_t stream, void *split_ws) {
@@ -359,13 +368,16 @@ dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *k
     const int resident = sp.nsplit > 1 ? resident_pairs<dsa::mla8::sparse_mla_fp8_kernel<true>, C::THREADS, C::SMEM>()
                                        : resident_pairs<dsa::mla8::sparse_mla_fp8_kernel<false>, C::THREADS, C::SMEM>();
     if (resident <= 0) return DSA_ERR_CUDA;
-    const unsigned grid = 2u * (unsigned)(units < resident ? units : resident);
+    const int pairs = resident < MLA_PAIRS ? resident : MLA_PAIRS;   // (an image of q for each)
+    const unsigned grid = 2u * (unsigned)(units < pairs ? units : pairs);
+    const auto *qr = static_cast<const __nv_bfloat16 *>(q);
+    auto *images = static_cast<unsigned char *>(split_ws) + mla_split_bytes(p);
     auto *ob = reinterpret_cast<__nv_bfloat16 *>(out);
     const auto *sc = static_cast<const unsigned char *>(kv_scale);
     if (sp.nsplit > 1)
-        dsa::mla8::sparse_mla_fp8_kernel<true><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, ob, lse, sp);
+        dsa::mla8::sparse_mla_fp8_kernel<true><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, qr, images, ob, lse, sp);
     else
-        dsa::mla8::sparse_mla_fp8_kernel<false><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, ob, lse, sp);
+        dsa::mla8::sparse_mla_fp8_kernel<false><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, qr, images, ob, lse, sp);
     dsa_status_t st = launch_status();
     if (st != DSA_OK || sp.nsplit < 2) return st;
     dsa::mla::combine_splits_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
@@ -874,7 +886,7 @@ dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, 
 
 size_t dsa_sparse_mla_fp8_workspace_size(const dsa_problem_t *p) {
     if (check_problem(p) != DSA_OK) return 0;
-    return mla_split_bytes(p);
+    return mla_split_bytes(p) + mla_fp8_image_bytes(p);
 }
 
 dsa_status_t dsa_sparse_mla_fp8_fwd(const dsa_problem_t *p, const void *q, const void *kv, const void *kv_scale,

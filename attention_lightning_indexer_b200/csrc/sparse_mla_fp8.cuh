@@ -40,8 +40,9 @@
 //          heads 64 c .. + 63 in CTA c), K = 256 keys: 32 MMAs
 // with a 7-slot ring of 16 KB atoms (128 keys x 128 codes, tile::gather4, 128-byte swizzle) in
 // MMA order QK_0, QK_1, PV_0, QK_2, PV_1, ...: five atoms for QK_b, four for PV_b (i = 0, 1 and
-// key half h = 0, 1).  A masked slot gathers a visible row of its token, so what lies in other
-// rows never enters a sum.
+// key half h = 0, 1).  The order runs on across units: the next unit's QK_0 stands before a
+// unit's last PV, so that the softmax need not wait between them.  A masked slot gathers a
+// visible row of its token, so what lies in other rows never enters a sum.
 //
 // Probabilities: the reference maximum m[h] moves when a block maximum exceeds it by more than
 // TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and half its smallest step, 2^-10, is 2^-14 of
@@ -50,18 +51,22 @@
 // hardly any block moves, 553, and half its smallest step would be 2^-11 of the largest p.  The
 // sum l takes p itself in fp32.
 //
-// Measured: 1024 queries x 2048 keys 565 us (tensor floor 354 us; the bf16 form 961 us), 64
-// queries 51 us (floor 22; bf16 85), one query over 8 pairs 20 us.  A block takes 4.2 us with 64
+// Measured: 1024 queries x 2048 keys 553 us (tensor floor 354 us; the bf16 form 961 us), 64
+// queries 50 us (floor 22; bf16 85), one query over 8 pairs 20 us.  A block takes 4.2 us with 64
 // pairs at work and 5.0 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
 // 512 bytes per CTA at 12 ns; and shared memory 7600 of 9700 cycles: tensor cores 3456
 // wavefronts, loads and stores 2270 to 2990, gathers 1152.  The chain QK, maxima, their exchange,
 // P', PV has no slack beside those: shortening one link moved the time by at most 2 %.
 //
 // Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
-// prepare (warp 8 also publishes each unit's block count and loads its q: the raw bf16 rows
-// land in q_s and are split in place into hi and lo, each head at its own power of two; then
+// prepare (warp 8 also publishes each unit's block count; they split q into hi and lo, each head
+// at its own power of two: the first unit's in place in q_s, a later one's while q_s is in use,
+// into an image in the workspace that is copied to q_s as soon as the last QK has read it; then
 // they fetch the scales of the keys of each block, up to four blocks ahead, and write the
 // previous unit's output), 12-19 softmax: TMEM lane quarter w % 4, head half (w - 12) / 4.
+//
+// The roles together are as much code as the instruction caches hold: what is not worth being
+// unrolled is rolled, and the waits are short (1024 queries: 583 us before both, 553 after).
 #pragma once
 
 #include <type_traits>
@@ -82,7 +87,8 @@ struct Cfg {
     static constexpr int NQ = 9;                    // raw: 9 x 64 dims; split: 4 hi, 4 lo, [RoPE hi | lo]
     static constexpr int NSLOT = 7, NLOAD = 7;
     static constexpr int NINFO = 4;                 // blocks of key scales kept ahead
-    static constexpr int NQS = 3;                   // units of q scales kept
+    static constexpr int NQS = 4;                   // units of q scales kept
+    static constexpr int QIMG = NQ * QATOM;         // bytes of a CTA's split q
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_PH = OFF_Q + NQ * QATOM;           // P' hi [256 keys][64 heads]
     static constexpr int OFF_PL = OFF_PH + 256 * 64;            // P' lo
@@ -99,15 +105,15 @@ struct Cfg {
     static constexpr int OFF_MV = OFF_FO + 2 * 128 * 4;         // [4] u32, heads whose reference moved
     static constexpr int OFF_BAR = OFF_MV + 16;
     // empty[7] pfull[7] q_raw q_ready q_free s_full[2] s_free[2] p_full pv_done o_ready xbar[2] lbar
-    // drain unit_full[2] unit_free[2] info_full[4] info_free[4] p_in fo_full[2] o_free qs_full[3]
-    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO + 1 + 3 + NQS;
+    // drain unit_full[2] unit_free[2] info_full[4] info_free[4] p_in fo_full[2] o_free qs_full[4] img_full
+    static constexpr int NBARS = 2 * NSLOT + 3 + 2 + 2 + 3 + 2 + 2 + 2 + 2 + 2 * NINFO + 1 + 3 + NQS + 1;
     // [0] TMEM base, [1] abort, [2..3] unit blocks, [4..5] unit fallback keys, [6] peer's abort flag
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
     static constexpr int OFF_LASTPOS = OFF_MISC + 32;           // even CTA: [2][NSLOT] last ring position issued
     static constexpr int SMEM = OFF_LASTPOS + 2 * NSLOT * 4;
     static constexpr int PREP0 = 8, SOFT0 = 12, WARPS = 20, THREADS = 32 * WARPS;
-    // of the 640 x 96 registers of the launch: 256 x 64 + 128 x 72 + 256 x 136 = 60,416
-    static constexpr int REG_LOAD = 64, REG_PREP = 72, REG_SOFT = 136;
+    // all of the 640 x 96 registers of the launch: 256 x 64 + 128 x 80 + 256 x 136 = 61,440
+    static constexpr int REG_LOAD = 64, REG_PREP = 80, REG_SOFT = 136;
     static constexpr int TMEM_S = 0, TMEM_O = 256;
     static constexpr float TAU = 4.8f;              // lazy-rescale threshold (log2 units)
     static constexpr int BASE = 4;                  // 2^(TAU + BASE) = 446 < 448
@@ -156,6 +162,24 @@ __device__ __forceinline__ void split_e4m3(__half2 x, uint32_t &hi, uint32_t &lo
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, LO);
 }
 
+// Bounded waits (a try suspends for a while by itself: seconds in all) that raise no error: the
+// role that gives up does, when it stops the pair.  The 60 waits of the kernel with the clock and
+// the error flag at each of them were enough code to miss in the instruction caches (583 us
+// instead of 556 for 1024 queries).
+constexpr int WAIT_TRIES = 1 << 22;
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i)
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i)
+        if (sm100::mbar_try_wait_cluster(bar, parity)) return true;
+    return false;
+}
+
 struct Unit {
     int nblocks;
     int fallback;   // a visible key of the token (position within its sequence)
@@ -195,6 +219,7 @@ template <bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, Problem P,
                       const unsigned char *__restrict__ kv_scale, const int32_t *__restrict__ idx,
+                      const __nv_bfloat16 *__restrict__ q_rows, unsigned char *__restrict__ q_images,
                       __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, mla::SplitArgs sp) {
     using C = Cfg;
     using namespace sm100;
@@ -246,6 +271,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     auto fo_full = [&](int i) { return p_in + 8 + 8u * i; }; // a unit's output factors are in place
     const uint32_t o_free = p_in + 24;                       // even CTA: O^T of both CTAs read out
     auto qs_full = [&](int i) { return p_in + 32 + 8u * i; };   // a unit's q scales are in place
+    const uint32_t img_full = p_in + 32 + 8u * C::NQS;       // the next unit's split q is in q_images
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
     volatile int *unit_nb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
     volatile int *unit_fb = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);
@@ -272,6 +298,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         mbar_init(fo_full(1), 4);
         mbar_init(o_free, 8);             // 4 preparing warps of each CTA
         for (int i = 0; i < C::NQS; ++i) mbar_init(qs_full(i), 4);   // own preparing warps (and the peer's bytes)
+        mbar_init(img_full, 4);           // preparing warps
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(lbar, 1);
@@ -299,6 +326,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (tid == 0 && tmem != 0) raise_error(ERR_SMEM_ALIGN);
     const uint32_t peer_misc1 = mapa_shared(sbase + C::OFF_MISC + 4, (uint32_t)peer);
     auto abort_pair = [&]() {                                // stop both CTAs of the pair
+        raise_error(ERR_WAIT_TIMEOUT);
         misc[1] = 1;
         st_cluster_u32(peer_misc1, 1u);
     };
@@ -311,77 +339,74 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint32_t lead_pfull = mapa_shared(pfull(lw), 0);
         const uint32_t slot_s = ring_s + lw * C::ATOM;
         if (lw == 0 && lane == 0) prefetch_tmap(&tm_kv);
+        struct Ctx {                                         // a unit as its gathers see it
+            RowInfo ri;
+            const int32_t *irow;                             // its slots and how many there are
+            int left, fb;
+        };
         bool ok = run;
-        int p = 0;                                           // ring position, counted across units
-        int last_issued = -1;
-        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
-            const int t = T - 1 - u / nsplit;
-            const int split = u % nsplit;
-            const RowInfo ri = row_info_warp(P, t);
-            const bool got = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
-            const int nblocks = got ? unit_nb[j & 1] : 0;
-            const int fb = got ? unit_fb[j & 1] : 0;
-            if (!__all_sync(0xffffffffu, got)) {
-                ok = false;
-                break;
+        int away = lw;                                       // ring positions up to this warp's next one (mod 7)
+        int uses = 0;                                        // of this warp's slot
+        // This warp's atom of the group, if it has one: value or key atom a, key half `half` of block b
+        auto gather = [&](const Ctx &c, int b, int half, int a) {
+            const int s0 = C::BLK * b + 128 * half + 4 * lane;
+            int4 x;
+            if ((K & 3) == 0 && s0 + 3 < c.left) {
+                x = __ldg(reinterpret_cast<const int4 *>(c.irow + s0));
+            } else {
+                x.x = s0 < c.left ? __ldg(c.irow + s0) : -1;
+                x.y = s0 + 1 < c.left ? __ldg(c.irow + s0 + 1) : -1;
+                x.z = s0 + 2 < c.left ? __ldg(c.irow + s0 + 2) : -1;
+                x.w = s0 + 3 < c.left ? __ldg(c.irow + s0 + 3) : -1;
             }
-            if (lane == 0) mbar_arrive(unit_free(j & 1));
-            if (nblocks == 0) continue;
-            // All atoms of a group gather the same rows; each lane loads the index entries of the
-            // next group while the current one is issued.
-            const int32_t *irow_s = idx + (int64_t)t * K + split * bps * C::BLK;
-            const int ks_left = K - split * bps * C::BLK;
-            auto entries = [&](int b, int h) {               // raw entries of this lane's 4 slots
-                const int s0 = C::BLK * b + 128 * h + 4 * lane;
-                int4 x;
-                if ((K & 3) == 0 && s0 + 3 < ks_left) {
-                    x = __ldg(reinterpret_cast<const int4 *>(irow_s + s0));
-                } else {
-                    x.x = s0 < ks_left ? __ldg(irow_s + s0) : -1;
-                    x.y = s0 + 1 < ks_left ? __ldg(irow_s + s0 + 1) : -1;
-                    x.z = s0 + 2 < ks_left ? __ldg(irow_s + s0 + 2) : -1;
-                    x.w = s0 + 3 < ks_left ? __ldg(irow_s + s0 + 3) : -1;
-                }
-                return x;
-            };
-            auto row_of = [&](int e) { return key_row(P, ri, mla::pair_visible(e, ri) ? e : fb); };
-            // group g needs key half cr of block b (QK_b, kept in e0) or both halves (PV_b)
-            int4 e0 = entries(0, cr), e1 = make_int4(-1, -1, -1, -1);
-            for (int g = 0; ok && g < 2 * nblocks; ++g) {
-                bool qk;
-                int b;
-                mla::pair_group(g, nblocks, qk, b);
-                int4 n0 = e0, n1 = e1;
-                if (g + 1 < 2 * nblocks) {
-                    bool qk1;
-                    int b1;
-                    mla::pair_group(g + 1, nblocks, qk1, b1);
-                    n0 = entries(b1, qk1 ? cr : 0);
-                    if (!qk1) n1 = entries(b1, 1);
-                }
+            auto row_of = [&](int e) { return key_row(P, c.ri, mla::pair_visible(e, c.ri) ? e : c.fb); };
+            const int r0 = row_of(x.x), r1 = row_of(x.y), r2 = row_of(x.z), r3 = row_of(x.w);
+            bool okw = true;
+            if (lane == 0) {
+                if (uses > 0) okw = wait(empty(lw), (uses - 1) & 1);
+                if (okw && cr == 0) mbar_expect_tx(pfull(lw), 2 * C::ATOM);   // both CTAs' rows
+            }
+            if (!__shfl_sync(0xffffffffu, okw, 0) || misc[1]) return false;
+            tma_gather4_pair(slot_s + 512 * lane, &tm_kv, lead_pfull, 128 * a, r0, r1, r2, r3);
+            ++uses;
+            return true;
+        };
+        Ctx cur = {}, old = {};
+        int nb = 0, b = 0, old_b = -1;                       // the current block and the one whose PV is due
+        for (int j = -1, u = pair0 - npairs; ok;) {
+            bool have = true;                                // another block, of this unit or a later one
+            for (++b; have && ok && b >= nb; ) {
+                ++j;
+                u += npairs;
+                have = u < units;
+                if (!have) break;
+                const int t = T - 1 - u / nsplit;
+                const int first = (u % nsplit) * bps * C::BLK;
+                cur.ri = row_info_warp(P, t);
+                cur.irow = idx + (int64_t)t * K + first;
+                cur.left = K - first;
+                const bool got = wait(unit_full(j & 1), (j >> 1) & 1);
+                nb = got ? unit_nb[j & 1] : 0;
+                cur.fb = got ? unit_fb[j & 1] : 0;
+                ok = __all_sync(0xffffffffu, got);
+                if (ok && lane == 0) mbar_arrive(unit_free(j & 1));
+                b = 0;
+            }
+            if (!ok) break;
+            // QK_b needs the CTA's own key half; PV of the block before: instruction i = m >> 1, key half
+            // m & 1.  (One copy of the code for both: the instruction caches are short.)
+#pragma unroll 1
+            for (int part = have ? 0 : 1; ok && part < (old_b >= 0 ? 2 : 1); ++part) {
+                const bool qk = part == 0;
                 const int natoms = qk ? C::QK_ATOMS : C::PV_ATOMS;
-                for (int m = 0; m < natoms; ++m) {
-                    const int pp = p + m;
-                    if (pp % C::NLOAD != lw) continue;
-                    const int4 x = (!qk && (m & 1)) ? e1 : e0;
-                    const int a = qk ? m : (m & 2) + cr;     // PV: instruction i = m >> 1, key half m & 1
-                    const int r0 = row_of(x.x), r1 = row_of(x.y), r2 = row_of(x.z), r3 = row_of(x.w);
-                    bool okw = true;
-                    if (lane == 0) {
-                        if (pp >= C::NSLOT) okw = mbar_wait(empty(lw), ((pp / C::NSLOT) - 1) & 1);
-                        if (okw && cr == 0) mbar_expect_tx(pfull(lw), 2 * C::ATOM);   // both CTAs' rows
-                    }
-                    if (!__shfl_sync(0xffffffffu, okw, 0) || misc[1]) {
-                        ok = false;
-                        break;
-                    }
-                    tma_gather4_pair(slot_s + 512 * lane, &tm_kv, lead_pfull, 128 * a, r0, r1, r2, r3);
-                    last_issued = pp;
-                }
-                e0 = n0;
-                e1 = n1;
-                p += natoms;
+                if (away < natoms)
+                    ok = gather(qk ? cur : old, qk ? b : old_b, qk ? cr : away & 1, qk ? away : (away & 2) + cr);
+                away -= natoms;
+                away += away < 0 ? C::NLOAD : 0;
             }
+            if (!have) break;
+            old = cur;
+            old_b = b;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) abort_pair();
@@ -389,19 +414,19 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // after an abort
         if (lane == 0)
             st_cluster_u32(mapa_shared(sbase + C::OFF_LASTPOS + 4u * (uint32_t)(cr * C::NSLOT + lw), 0),
-                           (uint32_t)last_issued);
+                           (uint32_t)(uses > 0 ? (uses - 1) * C::NSLOT + lw : -1));
     } else if (lane == 0 && cr == 1) {
         // ------------------------------------------------ relay (odd CTA): the peer's rows of P'^T
         const uint32_t p_full_lead = mapa_shared(p_full, 0);
         bool ok = run;
         int gb = 0;
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
-            ok = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+            ok = wait(unit_full(j & 1), (j >> 1) & 1);
             const int nblocks = ok ? unit_nb[j & 1] : 0;
             if (ok) mbar_arrive(unit_free(j & 1));
             for (int b = 0; ok && b < nblocks; ++b, ++gb) {
                 mbar_expect_tx(p_in, 128 * 128);
-                ok = mbar_wait_cluster(p_in, gb & 1) && !misc[1];
+                ok = wait_cluster(p_in, gb & 1) && !misc[1];
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive_remote(p_full_lead);
             }
@@ -420,112 +445,118 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         bool ok = run;
         bool issued = false;
         int slot = 0, phase = 0;                             // ring slot and its phase
-        int gb0 = 0;                                         // blocks of the earlier units
-        int nq = 0;                                          // units with blocks so far
-        for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
-            if (!__all_sync(0xffffffffu, mbar_wait(unit_full(j & 1), (j >> 1) & 1))) {
-                ok = false;
-                break;
-            }
-            const int nblocks = __shfl_sync(0xffffffffu, unit_nb[j & 1], 0);
-            if (elect_one()) mbar_arrive(unit_free(j & 1));
-            if (nblocks == 0) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait(q_ready, nq & 1))) {
-                ok = false;
-                break;
-            }
-            for (int g = 0; ok && g < 2 * nblocks; ++g) {
-                bool qk;
-                int b;
-                mla::pair_group(g, nblocks, qk, b);
-                const int gb = gb0 + b;
-                if (qk) {                                    // QK_b -> S^T buffer gb & 1
-                    bool okw = gb < 2 || mbar_wait(s_free(gb & 1), ((gb >> 1) - 1) & 1);
-                    tc_fence_after();
-                    const uint32_t d = C::TMEM_S + 128 * (gb & 1);
-#pragma unroll
-                    for (int a = 0; a < C::QK_ATOMS; ++a) {
-                        okw = okw && mbar_wait(pfull(slot), phase);
-                        // q: hi and lo atoms of the same 128 dims; for the RoPE atom [hi | lo] of the
-                        // keys, 64 dims of q hi and lo twice
-                        constexpr int ROPE = C::QK_ATOMS - 1;
-                        const uint64_t da = da_k + (uint64_t)(slot * (C::ATOM >> 4));
-                        const uint64_t qh = dq + (uint64_t)((a == ROPE ? 8 : a) * (C::QATOM >> 4));
-                        const uint64_t ql = a == ROPE ? qh + 4 : dq + (uint64_t)((4 + a) * (C::QATOM >> 4));
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const int qo = 2 * (a == ROPE ? (kk & 1) : kk);
-                                mma_f8_pair(d, da + 2 * kk, qh + qo, idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
-                                mma_f8_pair(d, da + 2 * kk, ql + qo, idesc_qk_lo, 1u);
-                            }
-                            mma_commit_pair_both(empty(slot));
-                        }
-                        if (++slot == C::NSLOT) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (elect_one()) {
-                        if (b == nblocks - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
-                        mma_commit_pair_both(s_full(gb & 1));
-                    }
-                    issued = true;
-                    if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
-                } else {                                     // PV_b
-                    // the four atoms first: they landed long before P'^T as a rule
-                    bool okw = true;
-                    int sl = slot, ph = phase;
-#pragma unroll
-                    for (int m = 0; m < C::PV_ATOMS; ++m) {
-                        okw = okw && mbar_wait(pfull(sl), ph);
-                        if (++sl == C::NSLOT) {
-                            sl = 0;
-                            ph ^= 1;
-                        }
-                    }
-                    if (elect_one()) mbar_expect_tx(p_in, 128 * 128);
-                    // the previous unit's O^T has been read out
-                    if (b == 0 && nq > 0) okw = okw && mbar_wait(o_free, (nq - 1) & 1);
-                    okw = okw && mbar_wait_cluster(p_full, gb & 1) && mbar_wait_cluster(p_in, gb & 1);
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-#pragma unroll
-                    for (int m = 0; m < C::PV_ATOMS; ++m) {
-                        const uint32_t d = C::TMEM_O + 128 * (m >> 1);
-                        const uint64_t da = da_mn + (uint64_t)(slot * (C::ATOM >> 4));
-                        const uint64_t db = dph + (uint64_t)((m & 1) * (128 * 64 >> 4));
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {    // 32 keys each
-                                mma_f8_pair(d, da + k * (4096 >> 4), db + k * (2048 >> 4), idesc_pv,
-                                            (b > 0 || (m & 1) || k > 0) ? 1u : 0u);
-                                mma_f8_pair(d, da + k * (4096 >> 4), db + ((C::OFF_PL - C::OFF_PH) >> 4) + k * (2048 >> 4),
-                                            idesc_pv, 1u);
-                            }
-                            mma_commit_pair_both(empty(slot));
-                        }
-                        if (++slot == C::NSLOT) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (elect_one()) {
-                        mma_commit_pair_both(pv_done);
-                        if (b == nblocks - 1) mma_commit_pair_both(o_ready);
-                    }
-                    issued = true;
-                    if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
+        int gb = -1, nq = -1;                                // current block and unit with blocks, counted over all units
+        int nb = 0, b = 0;                                   // blocks of the unit, the current one
+        int old_b = -1, old_gb = 0, old_q = 0;               // the block whose PV is due, its unit
+        bool old_last = false;
+        for (int j = -1, u = pair0 - npairs; ok;) {
+            bool have = true;                                // another block, of this unit or a later one
+            for (++b; have && ok && b >= nb; ) {
+                ++j;
+                u += npairs;
+                have = u < units;
+                if (!have) break;
+                ok = __all_sync(0xffffffffu, wait(unit_full(j & 1), (j >> 1) & 1));
+                nb = ok ? __shfl_sync(0xffffffffu, unit_nb[j & 1], 0) : 0;
+                if (ok && elect_one()) mbar_arrive(unit_free(j & 1));
+                b = 0;
+                if (nb > 0) {
+                    ++nq;
+                    ok = __all_sync(0xffffffffu, wait(q_ready, nq & 1));
                 }
             }
-            gb0 += nblocks;
-            ++nq;
+            if (!ok) break;
+            if (have) {                                      // QK_b -> S^T buffer gb & 1
+                ++gb;
+                bool okw = gb < 2 || wait(s_free(gb & 1), ((gb >> 1) - 1) & 1);
+                tc_fence_after();
+                const uint32_t d = C::TMEM_S + 128 * (gb & 1);
+#pragma unroll 1
+                for (int a = 0; a < C::QK_ATOMS; ++a) {
+                    okw = okw && wait(pfull(slot), phase);
+                    // q: hi and lo atoms of the same 128 dims; for the RoPE atom [hi | lo] of the
+                    // keys, 64 dims of q hi and lo twice
+                    constexpr int ROPE = C::QK_ATOMS - 1;
+                    const uint64_t da = da_k + (uint64_t)(slot * (C::ATOM >> 4));
+                    const uint64_t qh = dq + (uint64_t)((a == ROPE ? 8 : a) * (C::QATOM >> 4));
+                    const uint64_t ql = a == ROPE ? qh + 4 : dq + (uint64_t)((4 + a) * (C::QATOM >> 4));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const int qo = 2 * (a == ROPE ? (kk & 1) : kk);
+                            mma_f8_pair(d, da + 2 * kk, qh + qo, idesc_qk, (a > 0 || kk > 0) ? 1u : 0u);
+                            mma_f8_pair(d, da + 2 * kk, ql + qo, idesc_qk_lo, 1u);
+                        }
+                        mma_commit_pair_both(empty(slot));
+                    }
+                    if (++slot == C::NSLOT) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (elect_one()) {
+                    if (b == nb - 1) mma_commit_pair_both(q_free);   // the unit's last read of q_s
+                    mma_commit_pair_both(s_full(gb & 1));
+                }
+                issued = true;
+                if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
+            }
+            if (ok && old_b >= 0) {                          // PV of the block before
+                // the four atoms first: they landed long before P'^T as a rule
+                bool okw = true;
+                int sl = slot, ph = phase;
+#pragma unroll
+                for (int m = 0; m < C::PV_ATOMS; ++m) {
+                    okw = okw && wait(pfull(sl), ph);
+                    if (++sl == C::NSLOT) {
+                        sl = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (elect_one()) mbar_expect_tx(p_in, 128 * 128);
+                // the previous unit's O^T has been read out
+                if (old_b == 0 && old_q > 0) okw = okw && wait(o_free, (old_q - 1) & 1);
+                okw = okw && wait_cluster(p_full, old_gb & 1) && wait_cluster(p_in, old_gb & 1);
+                fence_proxy_async_smem();
+                tc_fence_after();
+#pragma unroll 1
+                for (int m = 0; m < C::PV_ATOMS; ++m) {
+                    const uint32_t d = C::TMEM_O + 128 * (m >> 1);
+                    const uint64_t da = da_mn + (uint64_t)(slot * (C::ATOM >> 4));
+                    const uint64_t db = dph + (uint64_t)((m & 1) * (128 * 64 >> 4));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {    // 32 keys each
+                            mma_f8_pair(d, da + k * (4096 >> 4), db + k * (2048 >> 4), idesc_pv,
+                                        (old_b > 0 || (m & 1) || k > 0) ? 1u : 0u);
+                            mma_f8_pair(d, da + k * (4096 >> 4), db + ((C::OFF_PL - C::OFF_PH) >> 4) + k * (2048 >> 4),
+                                        idesc_pv, 1u);
+                        }
+                        mma_commit_pair_both(empty(slot));
+                    }
+                    if (++slot == C::NSLOT) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (elect_one()) {
+                    mma_commit_pair_both(pv_done);
+                    if (old_last) mma_commit_pair_both(o_ready);
+                }
+                issued = true;
+                if (!__all_sync(0xffffffffu, okw && !misc[1])) ok = false;
+            }
+            if (!have) break;
+            old_b = b;
+            old_gb = gb;
+            old_q = nq;
+            old_last = b == nb - 1;
         }
         if (!ok) {
             if (lane == 0) abort_pair();
             if (issued) {                                    // nothing may be in flight at dealloc
                 if (elect_one()) mma_commit_pair_both(drain);
-                mbar_wait(drain, 0);
+                wait(drain, 0);
             }
         }
     }
@@ -541,15 +572,16 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         bool ok = run;
         int gb = 0;                                          // blocks so far
         int nq = 0;                                          // units with blocks so far
-        int nl = 0;                                          // q loads so far
+        int images = 0;                                      // units whose q went through the image
+        unsigned char *const image = q_images + (int64_t)blockIdx.x * C::QIMG;
         int qslot = 0;                                       // where the unit's q scales go
         // ---- epilogue of a unit (token pt, split ps, the pn-th with blocks): O^T times its output
         // factors into out.  These warps do it, so that the softmax goes on with the next unit; its
         // first PV waits for o_free.
         const uint32_t o_free_lead = mapa_shared(o_free, 0);
         auto epilogue = [&](int pt, int ps, int pn) {
-            bool fine = mbar_wait(fo_full(pn & 1), (pn >> 1) & 1);
-            fine = mbar_wait(o_ready, pn & 1) && fine;
+            bool fine = wait(fo_full(pn & 1), (pn >> 1) & 1);
+            fine = wait(o_ready, pn & 1) && fine;
             if (!__all_sync(0xffffffffu, fine)) return false;
             tc_fence_after();
             const float *f = fo + 128 * (pn & 1);
@@ -596,52 +628,53 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             int nblocks;
             bool okw = true;
             if (pw == 0) {
-                auto load_q = [&]() {
-                    mbar_expect_tx(q_raw, C::NQ * C::QATOM);
-                    for (int a = 0; a < C::NQ; ++a)
-                        tma_load_2d(q_s + a * C::QATOM, &tm_q, q_raw, 64 * a, t * 128 + 64 * cr);
-                };
                 // The first unit's q goes ahead of the gathers, which would queue before it in the copy
                 // engine (4.3 instead of 2 us); nothing holds q_s yet.
-                if (j == 0 && lane == 0) load_q();
+                if (j == 0 && lane == 0) {
+                    mbar_expect_tx(q_raw, C::QIMG);
+                    for (int a = 0; a < C::NQ; ++a) tma_load_2d(q_s + a * C::QATOM, &tm_q, q_raw, 64 * a, t * 128 + 64 * cr);
+                }
                 const Unit un = unit_scan(P, ri, irow, K, split, bps, lane);
                 nblocks = un.nblocks;
                 if (lane == 0) {
-                    if (j >= 2) okw = mbar_wait(unit_free(j & 1), ((j >> 1) - 1) & 1);
+                    if (j >= 2) okw = wait(unit_free(j & 1), ((j >> 1) - 1) & 1);
                     if (okw) {
                         unit_nb[j & 1] = nblocks;
                         unit_fb[j & 1] = un.fallback;
                         mbar_arrive(unit_full(j & 1));
                     }
-                    if (okw && nblocks > 0 && nq > 0) okw = mbar_wait(q_free, (nq - 1) & 1);
-                    if (okw && nblocks > 0 && j > 0) load_q();
                 }
                 okw = __shfl_sync(0xffffffffu, okw, 0);
-                nl += (j == 0 || (okw && nblocks > 0)) ? 1 : 0;
             } else {
-                okw = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+                okw = wait(unit_full(j & 1), (j >> 1) & 1);
                 nblocks = okw ? unit_nb[j & 1] : 0;
                 if (__all_sync(0xffffffffu, okw) && lane == 0) mbar_arrive(unit_free(j & 1));
             }
-            if (pw > 0) nl += (j == 0 || (okw && nblocks > 0)) ? 1 : 0;
             // every load is waited for, whatever happens to its unit: none is in flight at the end
-            if (j == 0 || nblocks > 0) okw = mbar_wait(q_raw, (nl - 1) & 1) && okw;
+            if (j == 0) okw = wait(q_raw, 0) && okw;
             if (!__all_sync(0xffffffffu, okw) || misc[1]) {
                 ok = false;
                 break;
             }
             if (nblocks == 0) continue;
-            // ---- split q in place: 8 lanes per head row, each the 16-byte chunk g of the row's nine
-            // 128-byte lines (dims 64 a + 8 g ..); the split row takes the same nine lines
+            // ---- split q: 8 lanes per head row, each the 16-byte chunk g of the row's nine 128-byte
+            // lines (dims 64 a + 8 g ..); the split row takes nine lines.  The first unit's in place in q_s,
+            // a later one's from its rows into the image while q_s is in use.
+            const bool in_place = j == 0;
+            unsigned char *const to = in_place ? smem + C::OFF_Q : image;
+            const unsigned char *const rows = in_place ? smem + C::OFF_Q
+                                                       : reinterpret_cast<const unsigned char *>(q_rows) + ((int64_t)t * 128 + 64 * cr) * 1152;
+            const int row_step = in_place ? 128 : 1152, line_step = in_place ? C::QATOM : 128;
             const int g8 = lane & 7;
 #pragma unroll 1
             for (int it = 0; it < 4; ++it) {
                 const int r = 16 * pw + 4 * it + (lane >> 3);
-                unsigned char *line = smem + C::OFF_Q + r * 128;
+                unsigned char *line = to + r * 128;
+                const unsigned char *raw = rows + r * row_step + ((g8 ^ (in_place ? r & 7 : 0)) << 4);
                 uint4 x[C::NQ];
 #pragma unroll
                 for (int a = 0; a < C::NQ; ++a)
-                    x[a] = *reinterpret_cast<const uint4 *>(line + a * C::QATOM + ((g8 ^ (r & 7)) << 4));
+                    x[a] = *reinterpret_cast<const uint4 *>(raw + a * line_step);
                 auto absmax = [](const uint4 &v, __nv_bfloat162 m) {
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -688,13 +721,35 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     st_async_f32(qsc_peer + 4u * at, s, qs_full_peer + 8u * qslot);
                 }
             }
-            fence_proxy_async_smem();
+            if (in_place) fence_proxy_async_smem();
+            else fence_proxy_async_global();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive_remote(q_ready_lead);
+                if (!in_place) mbar_arrive(img_full);
                 if (pw == 0) mbar_expect_tx(qs_full(qslot), 64 * 4);   // the scales of the peer's heads
                 else mbar_arrive(qs_full(qslot));
             }
+            if (!in_place) {                                 // into q_s once the unit before has read it
+                if (pw == 0) {
+                    if (lane == 0) {
+                        okw = wait(img_full, images & 1);
+                        if (okw && nq > 0) okw = wait(q_free, (nq - 1) & 1);
+                        if (okw) {
+                            fence_proxy_async_global();
+                            mbar_expect_tx(q_raw, C::QIMG);
+                            for (int a = 0; a < C::NQ; ++a) bulk_load(q_s + a * C::QATOM, image + a * C::QATOM, C::QATOM, q_raw);
+                        }
+                    }
+                    okw = __shfl_sync(0xffffffffu, okw, 0);
+                }
+                ++images;
+                if (okw) okw = wait(q_raw, images & 1);
+                if (!__all_sync(0xffffffffu, okw)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (lane == 0) mbar_arrive_remote(q_ready_lead);
             ++nq;
             qslot = qslot == C::NQS - 1 ? 0 : qslot + 1;
             // ---- scales of this CTA's keys (-1: masked) and the running largest exponent over both
@@ -717,7 +772,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const uint32_t top = max(c_own == 255u ? 0u : c_own, c_oth == 255u ? 0u : c_oth);
                 er = max(er, (int)__reduce_max_sync(0xffffffffu, top));
                 const int sl = gb & (C::NINFO - 1);
-                if (gb >= C::NINFO) okw = mbar_wait(info_free(sl), ((gb / C::NINFO) - 1) & 1);
+                if (gb >= C::NINFO) okw = wait(info_free(sl), ((gb / C::NINFO) - 1) & 1);
                 if (!__all_sync(0xffffffffu, okw) || misc[1]) {
                     ok = false;
                     break;
@@ -762,7 +817,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
             const int t = T - 1 - u / nsplit;
             const int split = u % nsplit;
-            const bool got = mbar_wait(unit_full(j & 1), (j >> 1) & 1);
+            const bool got = wait(unit_full(j & 1), (j >> 1) & 1);
             const int nblocks = got ? unit_nb[j & 1] : 0;
             if (named_bar_or(1, 256, !got || misc[1] != 0)) {
                 ok = false;
@@ -779,9 +834,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             for (int b = 0; b < nblocks; ++b) {
                 const int gb = gb0 + b;
                 const int sl = gb & (C::NINFO - 1);
-                const bool fail = misc[1] != 0 || !mbar_wait(info_full(sl), (gb / C::NINFO) & 1) ||
-                                  (b == 0 && !mbar_wait_cluster(qs_full(qslot), qphase)) ||
-                                  !mbar_wait(s_full(gb & 1), (gb >> 1) & 1);
+                const bool fail = misc[1] != 0 || !wait(info_full(sl), (gb / C::NINFO) & 1) ||
+                                  (b == 0 && !wait_cluster(qs_full(qslot), qphase)) ||
+                                  !wait(s_full(gb & 1), (gb >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 const float ks = info[128 * sl + key];
@@ -793,7 +848,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const uint32_t sb = t_lane + C::TMEM_S + 128 * (gb & 1) + 64 * h2;
                 const bool all_vis = __all_sync(0xffffffffu, vis);
                 // ---- block maxima of this CTA's keys (per head), then of the pair
-#pragma unroll
+#pragma unroll 1
                 for (int jj = 0; jj < 2; ++jj) {
                     uint32_t sr[32];
                     tmem_ld32(sb + 32 * jj, sr);
@@ -828,7 +883,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float q = qs[h];
                     if (b == 0) mq[mqh + 2] = q;
                     const float m_old = -mq[mqh];
-                    const bool okx = mbar_wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
+                    const bool okx = wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
                     const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * q;
                     const bool need = m_blk > m_old + C::TAU;
                     fs[h] = (need && m_old != -INFINITY) ? ex2_approx(m_old - m_blk) : 1.0f;
@@ -840,7 +895,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 named_bar(1, 256);
                 // the previous PV (this unit's or the last one's) has read P'^T and, for a rescale, O^T is whole
                 bool okp = true;
-                if (gb > 0) okp = mbar_wait(pv_done, (gb - 1) & 1);
+                if (gb > 0) okp = wait(pv_done, (gb - 1) & 1);
                 if (!okp) misc[1] = 1;
                 __syncwarp();
                 const uint4 mv = *reinterpret_cast<const uint4 *>(mvw);
@@ -959,7 +1014,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     st_async_f32(mapa_shared(sbase + C::OFF_XL + 4u * h, (uint32_t)peer), l_cta,
                                  mapa_shared(lbar, (uint32_t)peer));
                     if (st == 0) mbar_expect_tx(lbar, 128 * 4);
-                    const bool okl = mbar_wait_cluster(lbar, nq & 1);
+                    const bool okl = wait_cluster(lbar, nq & 1);
                     // the two CTAs add the same two numbers in the same order
                     const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
                     // O^T holds sum p 2^(e - er + BASE) code
@@ -1019,7 +1074,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (cr == 0 && run && tid < C::NSLOT) {
             const int *lp = reinterpret_cast<const int *>(smem + C::OFF_LASTPOS);
             const int pmax = max(lp[tid], lp[C::NSLOT + tid]);
-            if (pmax >= 0) mbar_wait_cluster(pfull(tid), (uint32_t)(pmax / C::NSLOT) & 1u);
+            if (pmax >= 0) wait_cluster(pfull(tid), (uint32_t)(pmax / C::NSLOT) & 1u);
         }
         cluster_sync();
     }

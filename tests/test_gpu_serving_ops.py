@@ -524,6 +524,24 @@ def test_attention_masks(T):
     _check_rows(q, codes, byte, rows, out, lse, range(min(T, 12)))
 
 
+@pytest.mark.parametrize("tail", [0, 90])
+def test_attention_rows_of_unlike_lengths_in_turn(tail):
+    """Several rows per SM pair, of 0 to 3 blocks: empty rows first, last and between, rows of one key."""
+    S, T, topk = 1500, 330, 700
+    codes, byte = _cache(S, seed=21)
+    q = _queries(T, seed=22)
+    pos = S - T + np.arange(T)
+    idx = _random_idx(T, topk, pos, seed=23)
+    keep = np.random.default_rng(24).choice([0, 0, 1, 200, 256, 257, 512, 513, 700], T)
+    keep[T - tail:] = 0                                     # the rows that are taken first
+    keep[:5] = [0, 700, 0, 1, 0]
+    idx[np.arange(topk)[None, :] >= keep[:, None]] = -1
+    out, lse = _run_mla(_packed(T, S, topk), q, codes, byte, dev(idx))
+    _check_rows(q, codes, byte, lambda t: idx[t][idx[t] >= 0], out, lse, range(0, T, 3), heads=slice(0, 128, 9))
+    again, lse2 = _run_mla(_packed(T, S, topk), q, codes, byte, dev(idx))
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_masked_rows_may_hold_anything():
     S, T, topk = 400, 90, 128
     codes, byte = _cache(S, seed=4)

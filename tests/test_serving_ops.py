@@ -208,6 +208,11 @@ def test_attention_workspace():
     assert _mla(small, ws=FAKE, ws_bytes=need - 1) == WORKSPACE
     assert _mla(small, ws=FAKE + 16, ws_bytes=need) == WORKSPACE
     assert dsa.load().dsa_sparse_mla_fp8_workspace_size(None) == 0
+    # many rows: the images of q of 74 pairs, however many rows there are
+    many = dsa.dsa_sparse_mla_fp8_workspace_size(_problem(total_q=1000, max_len_q=1000, total_k=4096, max_len_k=4096, topk=2048))
+    assert many == dsa.dsa_sparse_mla_fp8_workspace_size(_problem(total_q=4000, max_len_q=4000, total_k=4096, max_len_k=4096, topk=2048))
+    assert many == 74 * 2 * 9 * 64 * 128
+    assert dsa.dsa_sparse_mla_fp8_workspace_size(_problem(total_q=1, max_len_q=1, total_k=4096, max_len_k=4096, topk=256)) == 0
 
 
 def test_attention_reference_against_plain_softmax():
