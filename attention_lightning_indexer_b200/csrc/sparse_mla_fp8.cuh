@@ -48,15 +48,16 @@
 // TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and half its smallest step, 2^-10, is 2^-14 of
 // the largest p.  A move sends columns of O^T through registers (0.1 to 0.9 us of a block's 4 to
 // 5): 1024 queries took 621 us with TAU = 2.8 and BASE = 6, 565 with 4.8 and 4; 7.8 and 1, where
-// hardly any block moves, 553, and half its smallest step would be 2^-11 of the largest p.  The
-// sum l takes p itself in fp32.
+// hardly any block moves, takes 2 % less, and half its smallest step would be 2^-11 of the largest
+// p.  The sum l takes p itself in fp32.
 //
-// Measured: 1024 queries x 2048 keys 553 us (tensor floor 354 us; the bf16 form 961 us), 64
+// Measured: 1024 queries x 2048 keys 548 us (tensor floor 354 us; the bf16 form 961 us), 64
 // queries 50 us (floor 22; bf16 85), one query over 8 pairs 20 us.  A block takes 4.2 us with 64
-// pairs at work and 5.0 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
-// 512 bytes per CTA at 12 ns; and shared memory 7600 of 9700 cycles: tensor cores 3456
-// wavefronts, loads and stores 2270 to 2990, gathers 1152.  The chain QK, maxima, their exchange,
-// P', PV has no slack beside those: shortening one link moved the time by at most 2 %.
+// pairs at work and 4.7 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
+// 512 bytes per CTA at 12 ns; and shared memory 6800 of 9050 cycles: tensor cores 3456
+// wavefronts, loads and stores 2100, gathers 1152.  The chain QK, maxima, their exchange, P', PV
+// has no slack beside those, and the SM clock falls to 1.73 GHz: leaving out any one of the
+// gathers for PV, half of the QK or PV MMAs, or the split of P' saved 4 %.
 //
 // Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
 // prepare (warp 8 also publishes each unit's block count; they split q into hi and lo, each head
