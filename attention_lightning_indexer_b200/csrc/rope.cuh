@@ -35,8 +35,9 @@ constexpr int FULL_GRID = 148 * 8;   // CTAs that keep every SM busy
 // and 4 CTAs per SM, 64 with 3 CTAs, 59 with 2 heads and 5, 66 with 6, 69 with 1 and 7 (59 as a
 // copy without the rotation, with 3 CTAs; all with eight tokens per CTA).  5003 x 64 heads, half
 // layout: 39 us with 1 head and 5 CTAs, 42 with 6; before the streamed stores 45 against 50 with
-// 4 CTAs, 57 to 73 with 2 heads.
-__host__ __device__ constexpr int heads_in_flight(bool vec, bool interleaved) { return !vec ? 2 : interleaved ? 4 : 1; }
+// 4 CTAs, 57 to 73 with 2 heads.  Single pairs (2000 x 40 heads of 150 dims at odd strides, 48 MB,
+// interleaved): 22 us with 4 and 4 CTAs, 25 with 2, 27 with 6 CTAs, 37 without a bound on registers.
+__host__ __device__ constexpr int heads_in_flight(bool vec, bool interleaved) { return !vec || interleaved ? 4 : 1; }
 
 struct Args {
     const void *x;
@@ -75,7 +76,7 @@ __device__ __forceinline__ void store(T *p, const Vec<T, V> &v) {
 // in the interleaved one, one pair where V = 1) or the copy of V elements outside the
 // rotated part.  Threads beyond a whole number of heads idle.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(NT, V == 1 ? 1 : IL ? 4 : 5) rope_kernel(Args g) {
+__global__ void __launch_bounds__(NT, V == 1 || IL ? 4 : 5) rope_kernel(Args g) {
     constexpr int PER = IL ? (V == 1 ? 1 : V / 2) : V;       // pairs of a rotation item
     constexpr bool TWO = !IL || V == 1;                      // an item has a second vector
     constexpr int U = heads_in_flight(V > 1, IL);
