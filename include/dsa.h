@@ -409,7 +409,7 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * times its own, a key keeps 2^-14 of the largest probability's weight times 2^n.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd
  *   workspace : device, >= dsa_sparse_mla_fp8_workspace_size(p) bytes, 256-byte aligned (may
- *               be NULL when that is 0; at most 11 MB beyond a few query rows).  It holds the
+ *               be NULL when that is 0; at most 31 MB, 11 from 38 query rows on).  It holds the
  *               parts of rows that are split over several SM pairs when there are few query
  *               rows, and the queries that are next in turn when there are many: calls that
  *               share it must not overlap on the GPU (two captured graphs replayed at once
