@@ -61,8 +61,8 @@
 //
 // Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
 // prepare (warp 8 also publishes each unit's block count; they split q into hi and lo, each head
-// at its own power of two: the first unit's in place in q_s, a later one's while q_s is in use,
-// into an image in the workspace that is copied to q_s as soon as the last QK has read it; then
+// at its own power of two, while q_s is in use, into an image in the workspace that is copied to
+// q_s as soon as the last QK has read it (the first unit's q: the softmax warps, in place); then
 // they fetch the scales of the keys of each block, up to four blocks ahead, and write the
 // previous unit's output), 12-19 softmax: TMEM lane quarter w % 4, head half (w - 12) / 4.
 //
@@ -332,6 +332,69 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         st_cluster_u32(peer_misc1, 1u);
     };
 
+    const float sl2 = P.sm_scale * 1.4426950408889634f;
+    const uint32_t q_ready_lead = mapa_shared(q_ready, 0);
+    const uint32_t qsc_peer = mapa_shared(sbase + C::OFF_QS, (uint32_t)peer);
+    const uint32_t qs_full_peer = mapa_shared(qs_full(0), (uint32_t)peer);
+    // Split of q, head rows r0 .. r0 + 4 n - 1: 8 lanes per row, each the 16-byte chunk g of the row's nine
+    // 128-byte lines (dims 64 a + 8 g ..); the split row takes nine lines of `to`.  In place: the raw rows
+    // lie in q_s as TMA left them, else `rows` are rows of q.  scale(r, s) takes each row's scale in
+    // one of its lanes.
+    auto split_q = [&](auto in_place, unsigned char *to, const unsigned char *rows, int r0, int n, auto scale) {
+        const int row_step = in_place.value ? 128 : 1152, line_step = in_place.value ? C::QATOM : 128;
+        const int g8 = lane & 7;
+#pragma unroll 1
+        for (int it = 0; it < n; ++it) {
+            const int r = r0 + 4 * it + (lane >> 3);
+            unsigned char *line = to + r * 128;
+            const unsigned char *raw = rows + r * row_step + ((g8 ^ (in_place.value ? r & 7 : 0)) << 4);
+            uint4 x[C::NQ];
+#pragma unroll
+            for (int a = 0; a < C::NQ; ++a)
+                x[a] = *reinterpret_cast<const uint4 *>(raw + a * line_step);
+            auto absmax = [](const uint4 &v, __nv_bfloat162 m) {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+                return m;
+            };
+            __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+            for (int a = 0; a < 8; ++a) m = absmax(x[a], m);
+            const __nv_bfloat162 mr2 = absmax(x[8], __floats2bfloat162_rn(0.f, 0.f));
+            uint32_t top = max(max(cache::abs_bits(__low2float(m)), cache::abs_bits(__high2float(m))),
+                               max(cache::abs_bits(__low2float(mr2) * cache::KV8_ROPE_GAIN),
+                                   cache::abs_bits(__high2float(mr2) * cache::KV8_ROPE_GAIN)));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t byte = cache::scale_byte(top);
+            const float inv = cache::scale_inverse(byte);
+            __syncwarp();                                // the rows of this warp are read
+#pragma unroll
+            for (int a = 0; a < C::NQ; ++a) {
+                const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+                const float gain = a == 8 ? cache::KV8_ROPE_GAIN : 1.0f;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v0 = __uint_as_float(w[i] << 16), v1 = __uint_as_float(w[i] & 0xffff0000u);
+                    // fp16 holds the 8 significant bits of bf16 down to 2^-24
+                    split_e4m3<__NV_E5M2>(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
+                }
+                const uint2 h = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                const uint2 l = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                // line and 16-byte chunk of the split row: latent dims 128 A .. in atoms A and 4 + A,
+                // the RoPE dims in atom 8 as [hi | lo]
+                const int ah = a == 8 ? 8 : a >> 1, al = a == 8 ? 8 : 4 + (a >> 1);
+                const int ch = (a == 8 ? 0 : (a & 1) * 4) + (g8 >> 1), cl = a == 8 ? 4 + (g8 >> 1) : ch;
+                *reinterpret_cast<uint2 *>(line + ah * C::QATOM + ((ch ^ (r & 7)) << 4) + 8 * (g8 & 1)) = h;
+                *reinterpret_cast<uint2 *>(line + al * C::QATOM + ((cl ^ (r & 7)) << 4) + 8 * (g8 & 1)) = l;
+            }
+            if (g8 == 0) scale(r, ue8m0_to_float(byte) * sl2);
+        }
+    };
+
     if (warp < C::PREP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOAD));
     if (warp < C::NLOAD) {
@@ -565,10 +628,6 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_PREP));
         // ------------------------------------------------ units, q, key scales, output
         const int pw = warp - C::PREP0;
-        const float sl2 = P.sm_scale * 1.4426950408889634f;
-        const uint32_t q_ready_lead = mapa_shared(q_ready, 0);
-        const uint32_t qsc_peer = mapa_shared(sbase + C::OFF_QS, (uint32_t)peer);
-        const uint32_t qs_full_peer = mapa_shared(qs_full(0), (uint32_t)peer);
         if (pw == 0 && lane == 0) prefetch_tmap(&tm_q);
         bool ok = run;
         int gb = 0;                                          // blocks so far
@@ -658,80 +717,30 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 break;
             }
             if (nblocks == 0) continue;
-            // ---- split q: 8 lanes per head row, each the 16-byte chunk g of the row's nine 128-byte
-            // lines (dims 64 a + 8 g ..); the split row takes nine lines.  The first unit's in place in q_s,
-            // a later one's from its rows into the image while q_s is in use.
-            const bool in_place = j == 0;
-            unsigned char *const to = in_place ? smem + C::OFF_Q : image;
-            const unsigned char *const rows = in_place ? smem + C::OFF_Q
-                                                       : reinterpret_cast<const unsigned char *>(q_rows) + ((int64_t)t * 128 + 64 * cr) * 1152;
-            const int row_step = in_place ? 128 : 1152, line_step = in_place ? C::QATOM : 128;
-            const int g8 = lane & 7;
-#pragma unroll 1
-            for (int it = 0; it < 4; ++it) {
-                const int r = 16 * pw + 4 * it + (lane >> 3);
-                unsigned char *line = to + r * 128;
-                const unsigned char *raw = rows + r * row_step + ((g8 ^ (in_place ? r & 7 : 0)) << 4);
-                uint4 x[C::NQ];
-#pragma unroll
-                for (int a = 0; a < C::NQ; ++a)
-                    x[a] = *reinterpret_cast<const uint4 *>(raw + a * line_step);
-                auto absmax = [](const uint4 &v, __nv_bfloat162 m) {
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
-                    return m;
-                };
-                __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-                for (int a = 0; a < 8; ++a) m = absmax(x[a], m);
-                const __nv_bfloat162 mr2 = absmax(x[8], __floats2bfloat162_rn(0.f, 0.f));
-                uint32_t top = max(max(cache::abs_bits(__low2float(m)), cache::abs_bits(__high2float(m))),
-                                   max(cache::abs_bits(__low2float(mr2) * cache::KV8_ROPE_GAIN),
-                                       cache::abs_bits(__high2float(mr2) * cache::KV8_ROPE_GAIN)));
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const uint32_t byte = cache::scale_byte(top);
-                const float inv = cache::scale_inverse(byte);
-                __syncwarp();                                // the rows of this warp are read
-#pragma unroll
-                for (int a = 0; a < C::NQ; ++a) {
-                    const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-                    const float gain = a == 8 ? cache::KV8_ROPE_GAIN : 1.0f;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v0 = __uint_as_float(w[i] << 16), v1 = __uint_as_float(w[i] & 0xffff0000u);
-                        // fp16 holds the 8 significant bits of bf16 down to 2^-24
-                        split_e4m3<__NV_E5M2>(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
-                    }
-                    const uint2 h = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                    const uint2 l = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                    // line and 16-byte chunk of the split row: latent dims 128 A .. in atoms A and 4 + A,
-                    // the RoPE dims in atom 8 as [hi | lo]
-                    const int ah = a == 8 ? 8 : a >> 1, al = a == 8 ? 8 : 4 + (a >> 1);
-                    const int ch = (a == 8 ? 0 : (a & 1) * 4) + (g8 >> 1), cl = a == 8 ? 4 + (g8 >> 1) : ch;
-                    *reinterpret_cast<uint2 *>(line + ah * C::QATOM + ((ch ^ (r & 7)) << 4) + 8 * (g8 & 1)) = h;
-                    *reinterpret_cast<uint2 *>(line + al * C::QATOM + ((cl ^ (r & 7)) << 4) + 8 * (g8 & 1)) = l;
+            // ---- q of a later unit (the first one's: the softmax warps), from its rows into the image while
+            // q_s is in use
+            if (j > 0) {
+                // no unit had blocks: the softmax warps split the first one's q and scales all the same
+                if (nq == 0 && j == 1) okw = wait(unit_free(0), 0);
+                if (!__all_sync(0xffffffffu, okw)) {
+                    ok = false;
+                    break;
                 }
-                if (g8 == 0) {
-                    const int at = 128 * qslot + 64 * cr + r;
-                    const float s = ue8m0_to_float(byte) * sl2;
-                    qsc[at] = s;
-                    st_async_f32(qsc_peer + 4u * at, s, qs_full_peer + 8u * qslot);
+                split_q(std::false_type{}, image,
+                        reinterpret_cast<const unsigned char *>(q_rows) + ((int64_t)t * 128 + 64 * cr) * 1152, 16 * pw, 4,
+                        [&](int r, float s) {
+                            const int at = 128 * qslot + 64 * cr + r;
+                            qsc[at] = s;
+                            st_async_f32(qsc_peer + 4u * at, s, qs_full_peer + 8u * qslot);
+                        });
+                fence_proxy_async_global();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(img_full);
+                    if (pw == 0) mbar_expect_tx(qs_full(qslot), 64 * 4);   // the scales of the peer's heads
+                    else mbar_arrive(qs_full(qslot));
                 }
-            }
-            if (in_place) fence_proxy_async_smem();
-            else fence_proxy_async_global();
-            __syncwarp();
-            if (lane == 0) {
-                if (!in_place) mbar_arrive(img_full);
-                if (pw == 0) mbar_expect_tx(qs_full(qslot), 64 * 4);   // the scales of the peer's heads
-                else mbar_arrive(qs_full(qslot));
-            }
-            if (!in_place) {                                 // into q_s once the unit before has read it
-                if (pw == 0) {
+                if (pw == 0) {                               // into q_s once the unit before has read it
                     if (lane == 0) {
                         okw = wait(img_full, images & 1);
                         if (okw && nq > 0) okw = wait(q_free, (nq - 1) & 1);
@@ -749,8 +758,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     ok = false;
                     break;
                 }
+                if (lane == 0) mbar_arrive_remote(q_ready_lead);
             }
-            if (lane == 0) mbar_arrive_remote(q_ready_lead);
             ++nq;
             qslot = qslot == C::NQS - 1 ? 0 : qslot + 1;
             // ---- scales of this CTA's keys (-1: masked) and the running largest exponent over both
@@ -818,11 +827,37 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         for (int j = 0, u = pair0; ok && u < units; ++j, u += npairs) {
             const int t = T - 1 - u / nsplit;
             const int split = u % nsplit;
-            const bool got = wait(unit_full(j & 1), (j >> 1) & 1);
+            // The first unit's q is split here, where eight warps have nothing to do yet (2.4 us; the four
+            // preparing warps took 3.8, with the gathers' rows waiting).
+            bool got = true;
+            float q_scale[2] = {0.f, 0.f};
+            if (j == 0) {
+                got = wait(q_raw, 0);
+                if (__all_sync(0xffffffffu, got))
+                    split_q(std::true_type{}, smem + C::OFF_Q, smem + C::OFF_Q, 8 * (warp - C::SOFT0), 2, [&](int r, float s) {
+                        qsc[64 * cr + r] = s;
+                        if ((r & 4) == 0) q_scale[0] = s;
+                        else q_scale[1] = s;
+                    });
+                fence_proxy_async_smem();
+            }
+            got = wait(unit_full(j & 1), (j >> 1) & 1) && got;
             const int nblocks = got ? unit_nb[j & 1] : 0;
             if (named_bar_or(1, 256, !got || misc[1] != 0)) {
                 ok = false;
                 break;
+            }
+            if (j == 0 && nblocks > 0) {                     // what the preparing warps do for later units
+                if ((lane & 7) == 0) {
+                    const int at = 64 * cr + 8 * (warp - C::SOFT0) + (lane >> 3);
+                    st_async_f32(qsc_peer + 4u * at, q_scale[0], qs_full_peer);
+                    st_async_f32(qsc_peer + 4u * (at + 4), q_scale[1], qs_full_peer);
+                }
+                if (lane == 0 && warp < C::SOFT0 + 4) {
+                    mbar_arrive_remote(q_ready_lead);
+                    if (warp == C::SOFT0) mbar_expect_tx(qs_full(0), 64 * 4);
+                    else mbar_arrive(qs_full(0));
+                }
             }
             if (st == 0) mbar_arrive(unit_free(j & 1));
             const int mqh = (st >> 1) * 4 + (st & 1);        // st < 128: this thread's head in mq
