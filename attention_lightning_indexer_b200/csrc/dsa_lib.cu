@@ -380,7 +380,8 @@ dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *k
         dsa::mla8::sparse_mla_fp8_kernel<false><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, qr, images, ob, lse, sp);
     dsa_status_t st = launch_status();
     if (st != DSA_OK || sp.nsplit < 2) return st;
-    dsa::mla::combine_splits_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
+    static_assert(MLA_MAX_SPLITS <= dsa::mla8::MAX_SPLITS, "parts of a row");
+    dsa::mla8::combine_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
     return launch_status();
 }
 
