@@ -51,8 +51,8 @@
 // hardly any block moves, takes 2 % less, and half its smallest step would be 2^-11 of the largest
 // p.  The sum l takes p itself in fp32.
 //
-// Measured: 1024 queries x 2048 keys 548 us (tensor floor 354 us; the bf16 form 961 us), 64
-// queries 50 us (floor 22; bf16 85), one query over 8 pairs 20 us.  A block takes 4.2 us with 64
+// Measured: 1024 queries x 2048 keys 545 us (tensor floor 354 us; the bf16 form 961 us), 64
+// queries 49 us (floor 22; bf16 85), one query over 8 pairs 17 us with the merge.  A block takes 4.2 us with 64
 // pairs at work and 4.7 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
 // 512 bytes per CTA at 12 ns; and shared memory 6800 of 9050 cycles: tensor cores 3456
 // wavefronts, loads and stores 2100, gathers 1152.  The chain QK, maxima, their exchange, P', PV
