@@ -3,22 +3,25 @@
 // 576-d rows, the value is the 512-d latent.
 //   z[t,h,i] = sm_scale * q[t,h,:] . kv[idx[t,i], :]     out = softmax(z) . kv[:, 0:512]
 //
-// Eight bits on the tensor cores without losing the other operand's: a bf16 number has 8
-// significant bits and e4m3 has 4, so q (and a probability) is the sum of two 8-bit numbers,
-// hi = Q(x) and lo = Q(x - hi), and every product with a cached code is two kind::f8f6f4
+// Eight bits on the tensor cores: a bf16 number has 8 significant bits and e4m3 has 4, so q (and
+// a probability) is the sum of two 8-bit numbers, hi = Q(x), e4m3, and lo = Q(x - hi), e5m2,
+// and every product with a cached code is two kind::f8f6f4
 // MMAs, each at twice the bf16 rate: the tensor time of the bf16 form, but the cached rows go
 // from HBM into the MMA as they are.  Nothing is dequantised, the gathers move 144 KB per CTA and
 // block instead of 272 KB, and a ring slot holds 128 dims of a key instead of 64.
 //
-// q's lo is e5m2: x - hi is at most 8 units of x's last bit, so its 3 significant bits are enough
-// (1 .. 8 are all among them), and its range reaches 2^-16: q is exact down to 2^-6 of a range
-// that ends at 448, where an e4m3 lo was off by 2^-10 below 2^-2 (lse off by 1e-4 at the worst,
-// since 16 times the RoPE dims sets the range; 9e-6 now).  A probability has more than 8 bits; its
-// lo is e4m3 (2^-9 of the value; e5m2 with TAU = 7.8, BASE = 1 below: 2^-8, and 2 % faster).
+// lo is e5m2 for its range, which reaches 2^-16.  For q, x - hi is at most 8 units of x's last bit,
+// so 3 significant bits are enough (1 .. 8 are all among them): q is exact down to 2^-6 of a
+// range that ends at 448, where an e4m3 lo was off by 2^-10 below 2^-2 (lse off by 1e-4 at the
+// worst, since 16 times the RoPE dims sets the range; 9e-6 now).  A probability has more than 8
+// bits: hi + lo is within 2^-8 of it above 2^-6 (as bf16 is), within 2^-14 below, 3 bits below
+// 2^-10, and steps by 2^-16 at last.  An e4m3 lo is twice as near at the upper end but steps by
+// 2^-9: 2047 keys at e^-10 beside one of weight 1 (9 % of the sum) were lost or doubled.
 //
 // The row's scale 2^e leaves the sums: S^T[key, h] is over codes, and its thread (which owns
 // one key) multiplies by 2^e; for the values, the probability takes the scale with it, P' =
-// p 2^(e - er + BASE), er the largest scale exponent among the keys this unit has read so far.
+// p 2^(e - er + BASE), er the largest scale exponent among the keys this unit has read so far (of
+// which p's reference takes account: see Probabilities).
 // The RoPE dims are in the row as two codes of 64 dims at 16 times the row's scale, so q's
 // RoPE dims are taken 16 times: the K axis is 4 atoms of latent codes and one atom [hi | lo],
 // multiplied by the same 64 RoPE dims of q twice.
@@ -44,15 +47,21 @@
 // unit's last PV, so that the softmax need not wait between them.  A masked slot gathers a
 // visible row of its token, so what lies in other rows never enters a sum.
 //
-// Probabilities: the reference maximum m[h] moves when a block maximum exceeds it by more than
-// TAU; p <= 2^TAU, so P' <= 2^(TAU + BASE) < 448, and half its smallest step, 2^-10, is 2^-14 of
-// the largest p.  A move sends columns of O^T through registers (0.1 to 0.9 us of a block's 4 to
-// 5): 1024 queries took 621 us with TAU = 2.8 and BASE = 6, 565 with 4.8 and 4; 7.8 and 1, where
-// hardly any block moves, takes 2 % less, and half its smallest step would be 2^-11 of the largest
-// p.  The sum l takes p itself in fp32.
+// Probabilities: what is to be held well is the weight, a probability times its key's scale, so
+// the reference m[h] is one of score + e - er (log2).  It moves up when a block's maximum exceeds
+// it by more than TAU, so that P' <= 2^(TAU + BASE) < 448, and down when a block's maximum lies
+// more than DOWN below it: many light keys beside a heavy one (a sequence's first token, for
+// many heads) are then held as well as if it were not there, but for those in its own block.  In
+// every block the largest P' is 2^(BASE - DOWN) = 1 or more (2^BASE in the heaviest).  A move
+// sends columns of O^T through registers (0.1 to 0.9 us of a block's 4 to 5): 1024 queries took
+// 621 us with TAU = 2.8 and BASE = 6, 565 with 4.8 and 4 (both before DOWN); with DOWN = 4 they
+// take 566, with 6 555, without it 552 (scores of deviation 1.7, where it does little else).
+// DEPTH ends the way down (what is 2^-20 of the heaviest so far needs no more), and SPAN bounds e -
+// er from below, so that p and its sums stay below 2^60 whatever the scales.  The sum l takes p
+// itself in fp32.
 //
-// Measured: 1024 queries x 2048 keys 545 us (tensor floor 354 us; the bf16 form 961 us), 64
-// queries 49 us (floor 22; bf16 85), one query over 8 pairs 17 us with the merge.  A block takes 4.2 us with 64
+// Measured: 1024 queries x 2048 keys 566 us (tensor floor 354 us; the bf16 form 961 us), 64
+// queries 50 us (floor 22; bf16 85), one query over 8 pairs 18 us with the merge.  A block takes 4.2 us with 64
 // pairs at work and 4.7 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
 // 512 bytes per CTA at 12 ns; and shared memory 6800 of 9050 cycles: tensor cores 3456
 // wavefronts, loads and stores 2100, gathers 1152.  The chain QK, maxima, their exchange, P', PV
@@ -116,7 +125,10 @@ struct Cfg {
     // all of the 640 x 96 registers of the launch: 256 x 64 + 128 x 80 + 256 x 136 = 61,440
     static constexpr int REG_LOAD = 64, REG_PREP = 80, REG_SOFT = 136;
     static constexpr int TMEM_S = 0, TMEM_O = 256;
-    static constexpr float TAU = 4.8f;              // lazy-rescale threshold (log2 units)
+    static constexpr float TAU = 4.8f;              // log2 units: the reference moves up beyond this,
+    static constexpr float DOWN = 4.0f;             // down beyond this,
+    static constexpr float DEPTH = 20.0f;           // and no lower than this below the largest so far
+    static constexpr float SPAN = 24.0f;            // scales further below the largest count as this far in it
     static constexpr int BASE = 4;                  // 2^(TAU + BASE) = 446 < 448
     static constexpr int ER_MIN = BASE;             // exponent bytes below this count as this
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -154,13 +166,12 @@ __device__ __forceinline__ float warp_fmax(float v) {
     return r;
 }
 
-// Two fp16 numbers as hi = Q(x), e4m3, and lo = Q(x - hi), e4m3 or e5m2 (two codes each).
-template <__nv_fp8_interpretation_t LO>
-__device__ __forceinline__ void split_e4m3(__half2 x, uint32_t &hi, uint32_t &lo) {
+// Two fp16 numbers as hi = Q(x), e4m3, and lo = Q(x - hi), e5m2 (two codes each).
+__device__ __forceinline__ void split_8bit(__half2 x, uint32_t &hi, uint32_t &lo) {
     const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
     const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
     hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, LO);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E5M2);
 }
 
 // Bounded waits (a try that fails has suspended the warp for 1.5 us, measured: 0.2 s in all) that
@@ -379,7 +390,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 for (int i = 0; i < 4; ++i) {
                     const float v0 = __uint_as_float(w[i] << 16), v1 = __uint_as_float(w[i] & 0xffff0000u);
                     // fp16 holds the 8 significant bits of bf16 down to 2^-24
-                    split_e4m3<__NV_E5M2>(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
+                    split_8bit(__floats2half2_rn(v0 * gain * inv, v1 * gain * inv), hi[i], lo[i]);
                 }
                 const uint2 h = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
                 const uint2 l = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
@@ -502,6 +513,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint32_t idesc_qk = idesc_e4m3(256, 128);
         const uint32_t idesc_qk_lo = idesc_qk | (1u << 10);                         // B e5m2
         const uint32_t idesc_pv = idesc_e4m3(256, 128) | (1u << 15) | (1u << 16);   // A and B MN-major
+        const uint32_t idesc_pv_lo = idesc_pv | (1u << 10);                         // B e5m2
         // descriptors step by bytes / 16 in their low word
         const uint64_t dq = desc_sw128(q_s), da_k = desc_sw128(ring_s), da_mn = desc_sw128_mn(ring_s, C::ATOM);
         const uint64_t dph = desc_sw64_mn(ph_s);
@@ -593,7 +605,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             mma_f8_pair(d, da + k * (4096 >> 4), db + k * (2048 >> 4), idesc_pv,
                                         (old_b > 0 || (m & 1) || k > 0) ? 1u : 0u);
                             mma_f8_pair(d, da + k * (4096 >> 4), db + ((C::OFF_PL - C::OFF_PH) >> 4) + k * (2048 >> 4),
-                                        idesc_pv, 1u);
+                                        idesc_pv_lo, 1u);
                         }
                         mma_commit_pair_both(empty(slot));
                     }
@@ -867,6 +879,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll
             for (int i = 0; i < 32; ++i) l[i] = 0ull;
             int er = C::ER_MIN;
+            float m_top = -INFINITY, sunk = 0.f;             // st < 128: of this thread's head (below)
             for (int b = 0; b < nblocks; ++b) {
                 const int gb = gb0 + b;
                 const int sl = gb & (C::NINFO - 1);
@@ -883,7 +896,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 const bool vis = !(ks < 0.f);
                 const uint32_t sb = t_lane + C::TMEM_S + 128 * (gb & 1) + 64 * h2;
                 const bool all_vis = __all_sync(0xffffffffu, vis);
-                // ---- block maxima of this CTA's keys (per head), then of the pair
+                // the key's scale against the largest so far (log2)
+                const float de = fmaxf((float)((int)(__float_as_uint(ks) >> 23) - er_new), -C::SPAN);
+                // ---- block maxima of score + scale of this CTA's keys (per head), then of the pair
 #pragma unroll 1
                 for (int jj = 0; jj < 2; ++jj) {
                     uint32_t sr[32];
@@ -896,13 +911,15 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                     const float k1 = vis ? ks : 1.0f;
                     float4 *r4 = reinterpret_cast<float4 *>(red + quarter * 128 + 64 * h2 + 32 * jj);
+                    const float4 *q4 = reinterpret_cast<const float4 *>(qs + 64 * h2 + 32 * jj);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+                        const float4 q = q4[i];
                         float4 r;
-                        r.x = warp_fmax(__uint_as_float(sr[4 * i]) * k1);
-                        r.y = warp_fmax(__uint_as_float(sr[4 * i + 1]) * k1);
-                        r.z = warp_fmax(__uint_as_float(sr[4 * i + 2]) * k1);
-                        r.w = warp_fmax(__uint_as_float(sr[4 * i + 3]) * k1);
+                        r.x = warp_fmax(fmaf(__uint_as_float(sr[4 * i]) * k1, q.x, de));
+                        r.y = warp_fmax(fmaf(__uint_as_float(sr[4 * i + 1]) * k1, q.y, de));
+                        r.z = warp_fmax(fmaf(__uint_as_float(sr[4 * i + 2]) * k1, q.z, de));
+                        r.w = warp_fmax(fmaf(__uint_as_float(sr[4 * i + 3]) * k1, q.w, de));
                         if (lane == 0) r4[i] = r;
                     }
                 }
@@ -916,14 +933,21 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float m_cta = fmaxf(fmaxf(red[h], red[128 + h]), fmaxf(red[256 + h], red[384 + h]));
                     st_async_f32(xm_peer + 4u * (128 * (gb & 1) + h), m_cta, xbar_peer + 8u * (gb & 1));
                     if (st == 0) mbar_expect_tx(xbar(gb & 1), 128 * 4);
-                    const float q = qs[h];
-                    if (b == 0) mq[mqh + 2] = q;
+                    if (b == 0) mq[mqh + 2] = qs[h];
                     const float m_old = -mq[mqh];
                     const bool okx = wait_cluster(xbar(gb & 1), (gb >> 1) & 1);
-                    const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta) * q;
-                    const bool need = m_blk > m_old + C::TAU;
-                    fs[h] = (need && m_old != -INFINITY) ? ex2_approx(m_old - m_blk) : 1.0f;
-                    if (need) mq[mqh] = -m_blk;
+                    const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta);
+                    // the largest so far: what was seen before loses as much as the largest scale gained,
+                    // SPAN at most (`sunk` so far)
+                    const float gain = b == 0 ? 0.f : fminf((float)(er_new - er), C::SPAN - sunk);
+                    sunk += gain;
+                    m_top = fmaxf(m_top - gain, m_blk);
+                    // up where the block exceeds the reference by more than TAU, down where it lies more than
+                    // DOWN below (a block without a visible key, or with NaN only, changes nothing)
+                    const float m_new = fmaxf(m_blk, m_top - C::DEPTH);
+                    const bool need = m_blk > -INFINITY && (m_blk > m_old + C::TAU || m_new < m_old - C::DOWN);
+                    fs[h] = (need && m_old != -INFINITY) ? ex2_approx(m_old - m_new) : 1.0f;
+                    if (need) mq[mqh] = -m_new;
                     if (!okx) misc[1] = 1;
                     const uint32_t w = __ballot_sync(0xffffffffu, need);
                     if (lane == 0) mvw[warp - C::SOFT0] = b > 0 ? w : 0u;   // warp i: heads 32 i .. + 31
@@ -1002,7 +1026,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             const uint64_t p2 = pack_f32x2(p0, p1);
                             l[8 * v + i] = add_f32x2(l[8 * v + i], p2);
                             unpack_f32x2(mul_f32x2(p2, kf2), p0, p1);
-                            split_e4m3<__NV_E4M3>(__floats2half2_rn(p0, p1), hi[i], lo[i]);
+                            split_8bit(__floats2half2_rn(p0, p1), hi[i], lo[i]);
                         }
                         uint32_t h[4], g[4];
 #pragma unroll

@@ -404,9 +404,14 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * effect.
  * Accuracy: q and the probabilities enter the tensor cores as two 8-bit floats each.  q's
  * elements are exact down to 2^-13 of their head's largest (the RoPE dims counted 16 times) and
- * off by at most 2^-21 of it below; a probability keeps 8 significant bits.  Products are exact and sums are fp32.  A probability is held relative to
- * the largest scale among the keys its row has read so far: next to keys whose scale is 2^n
- * times its own, a key keeps 2^-14 of the largest probability's weight times 2^n.
+ * off by at most 2^-21 of it below.  Products are exact and sums are fp32.  A key's weight
+ * (its probability times its row's scale) is held relative to the largest weight among the 256
+ * slots of its block (slots 256 b ..): within 2^-8 of itself, as a bf16 probability is, down to
+ * 2^-6 of that one; below, within 2^-14 of that one, but no worse than an eighth of itself, down
+ * to 2^-14; and below 2^-17 it may be lost (each 2^-4 further down in the heaviest block so far).
+ * So light keys beside a heavy one lose bits only if they share its block.  A block whose heaviest
+ * key is below 2^-20 of the heaviest so far is held relative to 2^-20 of that one, and a scale
+ * that is below 2^-24 of the row's largest so far counts as 2^-24 of it here.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd
  *   workspace : device, >= dsa_sparse_mla_fp8_workspace_size(p) bytes, 256-byte aligned (may
  *               be NULL when that is 0; at most 31 MB, 11 from 38 query rows on).  It holds the
