@@ -240,6 +240,7 @@ dsa_status_t topk_launch(const dsa_problem_t *p, const float *scores, int64_t ld
 // pairs one token's index row is split over.
 constexpr int MLA_PAIRS = 74;
 constexpr int MLA_MAX_SPLITS = 8;
+static_assert(MLA_MAX_SPLITS <= dsa::mla::MAX_SPLITS, "parts of a row in combine_splits_kernel");
 
 // Splits of each token's index row for the gathered attention: one unit per token when
 // the tokens alone fill the SMs (prefill, large decode batches); otherwise several units
@@ -380,8 +381,7 @@ dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *k
         dsa::mla8::sparse_mla_fp8_kernel<false><<<grid, C::THREADS, C::SMEM, stream>>>(tq, tkv, to_dev(p), sc, idx, qr, images, ob, lse, sp);
     dsa_status_t st = launch_status();
     if (st != DSA_OK || sp.nsplit < 2) return st;
-    static_assert(MLA_MAX_SPLITS <= dsa::mla8::MAX_SPLITS, "parts of a row");
-    dsa::mla8::combine_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
+    dsa::mla::combine_splits_kernel<<<(unsigned)p->total_q * 128u, 128, 0, stream>>>(sp.nsplit, sp.o_part, sp.lse_part, ob, lse);
     return launch_status();
 }
 

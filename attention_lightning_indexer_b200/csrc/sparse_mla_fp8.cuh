@@ -1144,47 +1144,5 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
 }
 
-// Merges the parts of split rows as combine_splits_kernel does, in the same order, with all parts'
-// loads in flight at once (one query in 8 parts: 17.4 us in all, 18.4 with a round trip per part).
-// grid = T * 128 blocks of 128 threads (4 value dims each).
-constexpr int MAX_SPLITS = 8;
-__global__ void __launch_bounds__(128) combine_kernel(int nsplit, const float *__restrict__ o_part,
-                                                     const float *__restrict__ lse_part,
-                                                     __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    const int row = blockIdx.x;                              // t * 128 + h
-    const int64_t part = (int64_t)(row >> 7) * nsplit * 128 + (row & 127);   // part c: + 128 c
-    float l[MAX_SPLITS];
-    float4 v[MAX_SPLITS];
-#pragma unroll
-    for (int c = 0; c < MAX_SPLITS; ++c) {
-        if (c < nsplit) {
-            l[c] = lse_part[part + c * 128];
-            v[c] = reinterpret_cast<const float4 *>(o_part + (part + c * 128) * 512)[threadIdx.x];
-        }
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < MAX_SPLITS; ++c)
-        if (c < nsplit) m = fmaxf(m, l[c]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f;
-    if (m != -INFINITY) {
-#pragma unroll
-        for (int c = 0; c < MAX_SPLITS; ++c) {
-            if (c >= nsplit) continue;
-            const float w = l[c] == -INFINITY ? 0.f : expf(l[c] - m);
-            wsum += w;
-            acc.x = fmaf(w, v[c].x, acc.x);
-            acc.y = fmaf(w, v[c].y, acc.y);
-            acc.z = fmaf(w, v[c].z, acc.z);
-            acc.w = fmaf(w, v[c].w, acc.w);
-        }
-    }
-    const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
-    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
-    reinterpret_cast<uint2 *>(out + (int64_t)row * 512)[threadIdx.x] = *reinterpret_cast<const uint2 *>(o);
-    if (threadIdx.x == 0) lse[row] = m == -INFINITY ? -INFINITY : m + logf(wsum);
-}
-
 }  // namespace mla8
 }  // namespace dsa

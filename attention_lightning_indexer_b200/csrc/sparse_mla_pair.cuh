@@ -737,11 +737,11 @@ sparse_mla_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     const bool okl = mbar_wait_cluster(lbar, nq & 1);
                     // the two CTAs add the same two numbers in the same order
                     const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
-                    const bool fine = okl && l_tot > 0.f;
+                    const bool fine = okl && l_tot != 0.f;              // (a NaN stays one)
                     fs[h] = fine ? 1.0f / l_tot : 0.f;
                     if ((h >> 6) == cr) {
                         const float lv =
-                            okl ? (l_tot > 0.f ? (mr[h] + log2f(l_tot)) * 0.6931471805599453f : -INFINITY) : NAN;
+                            okl ? (l_tot != 0.f ? (mr[h] + log2f(l_tot)) * 0.6931471805599453f : -INFINITY) : NAN;
                         if (partial) sp.lse_part[pbase + h] = lv;
                         else lse[obase + h] = lv;
                     }
@@ -835,37 +835,53 @@ sparse_mla_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 
 // Merges the nsplit partial results of each (token, head): lse = log sum_c exp(lse_c),
 // out = sum_c exp(lse_c - lse) o_c, rounded once to bf16.  Splits without a visible slot
-// (lse_c = -inf) weigh 0; a row without any gives out = 0, lse = -inf.  grid = T * 128
-// blocks of 128 threads (4 value dims each).
+// (lse_c = -inf) weigh 0; a row without any gives out = 0, lse = -inf.  A NaN in any part's lse
+// (a NaN in q or in an attended row, or a pipeline that gave up) makes the row NaN; the maximum
+// alone would pass over it.  All parts' loads are in flight at once (one query in 8 parts over
+// the 8-bit cache: 17.4 us in all, 18.4 with a round trip per part).  grid = T * 128 blocks of
+// 128 threads (4 value dims each).
+constexpr int MAX_SPLITS = 8;
 __global__ void __launch_bounds__(128) combine_splits_kernel(int nsplit, const float *__restrict__ o_part,
                                                             const float *__restrict__ lse_part,
                                                             __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
     const int row = blockIdx.x;                              // t * 128 + h
-    const int t = row >> 7, h = row & 127;
+    const int64_t part = (int64_t)(row >> 7) * nsplit * 128 + (row & 127);   // part c: + 128 c
+    float l[MAX_SPLITS];
+    float4 v[MAX_SPLITS];
+#pragma unroll
+    for (int c = 0; c < MAX_SPLITS; ++c) {
+        if (c < nsplit) {
+            l[c] = lse_part[part + c * 128];
+            v[c] = reinterpret_cast<const float4 *>(o_part + (part + c * 128) * 512)[threadIdx.x];
+        }
+    }
     float m = -INFINITY;
-    for (int c = 0; c < nsplit; ++c) m = fmaxf(m, lse_part[((int64_t)t * nsplit + c) * 128 + h]);
+#pragma unroll
+    for (int c = 0; c < MAX_SPLITS; ++c)
+        if (c < nsplit) m = fmaxf(m, l[c]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f;
-    if (m != -INFINITY) {
-        for (int c = 0; c < nsplit; ++c) {
-            const int64_t pr = ((int64_t)t * nsplit + c) * 128 + h;
-            const float lc = lse_part[pr];
-            const float wgt = lc == -INFINITY ? 0.f : expf(lc - m);
-            wsum += wgt;
-            const float4 v = reinterpret_cast<const float4 *>(o_part + pr * 512)[threadIdx.x];
-            acc.x = fmaf(wgt, v.x, acc.x);
-            acc.y = fmaf(wgt, v.y, acc.y);
-            acc.z = fmaf(wgt, v.z, acc.z);
-            acc.w = fmaf(wgt, v.w, acc.w);
+    float wsum = 0.f, none = -INFINITY;
+    if (m == -INFINITY) {                                    // no part has a number: -inf each, or a NaN
+#pragma unroll
+        for (int c = 0; c < MAX_SPLITS; ++c)
+            if (c < nsplit) none += l[c];
+        acc.x = acc.y = acc.z = acc.w = none == -INFINITY ? 0.f : NAN;
+    } else {                                                 // (a NaN part makes the sums NaN)
+#pragma unroll
+        for (int c = 0; c < MAX_SPLITS; ++c) {
+            if (c >= nsplit) continue;
+            const float w = l[c] == -INFINITY ? 0.f : expf(l[c] - m);
+            wsum += w;
+            acc.x = fmaf(w, v[c].x, acc.x);
+            acc.y = fmaf(w, v[c].y, acc.y);
+            acc.z = fmaf(w, v[c].z, acc.z);
+            acc.w = fmaf(w, v[c].w, acc.w);
         }
     }
     const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
-    __nv_bfloat16 *o = out + (int64_t)row * 512 + 4 * threadIdx.x;
-    o[0] = __float2bfloat16_rn(acc.x * inv);
-    o[1] = __float2bfloat16_rn(acc.y * inv);
-    o[2] = __float2bfloat16_rn(acc.z * inv);
-    o[3] = __float2bfloat16_rn(acc.w * inv);
-    if (threadIdx.x == 0) lse[row] = m == -INFINITY ? -INFINITY : m + logf(wsum);
+    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+    reinterpret_cast<uint2 *>(out + (int64_t)row * 512)[threadIdx.x] = *reinterpret_cast<const uint2 *>(o);
+    if (threadIdx.x == 0) lse[row] = m == -INFINITY ? none : m + logf(wsum);
 }
 
 }  // namespace mla

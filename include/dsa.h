@@ -176,7 +176,8 @@ dsa_status_t dsa_indexer_topk_streaming(const dsa_problem_t *p, const void *q_id
  * over the slots i whose index satisfies 0 <= idx <= pos(t); every other slot (-1,
  * future or out-of-range positions) is masked, so causality holds for any input.
  * A row with no valid slot gets out = 0 and lse = -inf.  A repeated index counts once
- * per occurrence.
+ * per occurrence.  A NaN in a query head makes that head's out and lse NaN, one in an
+ * attended row those of every head that attends it.
  *   q   : [T, 128, 576] bf16     kv  : [S, 576] bf16     idx : [T, topk] int32
  *   out : [T, 128, 512] bf16 (round-to-nearest-even from fp32)   lse : [T, 128] fp32
  */
