@@ -102,6 +102,28 @@ __device__ __forceinline__ int key_row(const Problem &P, const RowInfo &r, int s
     return __ldg(tab + (pg < npg ? pg : 0)) * 64 + (s & 63);
 }
 
+// key_row for plain loads, which nothing else bounds: -1 for a row outside the key arrays, which a
+// block-table entry outside the pool or a cu_k beyond total_k would give.
+__device__ __forceinline__ int key_row_checked(const Problem &P, const RowInfo &r, int s) {
+    if (P.block_table == nullptr) {
+        const int row = r.kbase + s;
+        return (unsigned)row < (unsigned)P.total_k ? row : -1;
+    }
+    const int pg = s >> 6;
+    const int npg = (r.len_k + 63) >> 6;
+    const int page = __ldg(P.block_table + (int64_t)r.seq * P.max_pages + (pg < npg ? pg : 0));
+    return (unsigned)page < (unsigned)(P.total_k >> 6) ? page * 64 + (s & 63) : -1;
+}
+
+// First row of the page that holds key position s (a multiple of 64) of a paged cache, for a TMA
+// load; total_k for an entry outside the pool: the rows behind the last one load as zeros.
+__device__ __forceinline__ int page_row(const Problem &P, const RowInfo &r, int s) {
+    const int pg = s >> 6;
+    const int npg = (r.len_k + 63) >> 6;
+    const int page = __ldg(P.block_table + (int64_t)r.seq * P.max_pages + (pg < npg ? pg : 0));
+    return (int)min((unsigned)page, (unsigned)(P.total_k >> 6)) * 64;
+}
+
 // Number of visible keys of a row: keys 0..pos that exist in the sequence.
 __device__ __forceinline__ int visible_keys(const RowInfo &r) {
     int n = r.pos + 1;
@@ -114,7 +136,7 @@ __device__ unsigned int g_error_flag;
 
 __device__ __forceinline__ void raise_error(unsigned int code) { atomicOr(&g_error_flag, code); }
 
-constexpr unsigned ERR_BOUNDS = 4u;   // a debug-mode check found an inconsistent input
+constexpr unsigned ERR_BOUNDS = 4u;   // an inconsistent input (a row outside the caches; debug-mode checks)
 
 // Debug mode: the row's sequence must lie inside the key arrays (cu_q / cu_k consistent with
 // total_k and max_len_k, block-table pages inside total_k).  A row that fails is counted

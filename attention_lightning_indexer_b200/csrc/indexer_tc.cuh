@@ -217,8 +217,8 @@ indexer_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (P.block_table == nullptr) {
                     tma_load_2d(dst, &tm_k, k_full(s), a * 128 / C::EB, kbase + kk0);
                 } else {   // a 128-key tile is two pages of 64 rows (the map's box is 64 rows)
-                    tma_load_2d(dst, &tm_k, k_full(s), a * 128 / C::EB, key_row(P, rk, kk0));
-                    tma_load_2d(dst + 64 * 128, &tm_k, k_full(s), a * 128 / C::EB, key_row(P, rk, kk0 + 64));
+                    tma_load_2d(dst, &tm_k, k_full(s), a * 128 / C::EB, page_row(P, rk, kk0));
+                    tma_load_2d(dst + 64 * 128, &tm_k, k_full(s), a * 128 / C::EB, page_row(P, rk, kk0 + 64));
                 }
             }
         }
@@ -292,8 +292,13 @@ indexer_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int j = it / C::NSUB, h = it % C::NSUB;
             const int key = key0 + j * tstride * C::BM + row;
             float ks = 1.f;   // the key's scale, loaded before the accumulator wait
+            bool stray = false;   // a key without a row: zero codes, but some scale
             if (FP8 && key < nkeys_total) {
-                const int kr = key_row(P, rk, key);
+                // (one sequence without cu arrays: key < total_k by construction)
+                const int row_or_none = QG > 1 ? key_row(P, rk, key) : key_row_checked(P, rk, key);
+                const int kr = QG > 1 ? row_or_none : max(row_or_none, 0);
+                stray = QG == 1 && row_or_none < 0;
+                if (stray) raise_error(ERR_BOUNDS);
                 ks = P.ue8m0 ? ue8m0_to_float(__ldg(reinterpret_cast<const uint8_t *>(k_scale) + kr))
                              : __ldg(reinterpret_cast<const float *>(k_scale) + kr);
             }
@@ -375,7 +380,7 @@ indexer_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     const int q = h * C::QPI + qw0 + qi;
                     if (q < qcount && key <= pos0 + q && key < nkeys_total) {
                         const int t = t0 + q;
-                        const float v = FP8 ? res[qi] * ks : res[qi];
+                        const float v = FP8 ? (stray ? 0.f : res[qi] * ks) : res[qi];
                         const int col = MODE == SAMPLE ? j * C::BM + row : key;
                         scores[(int64_t)(t - row_begin) * ld + col] = v;
                     }

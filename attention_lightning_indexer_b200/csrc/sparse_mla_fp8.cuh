@@ -202,7 +202,7 @@ struct Unit {
 __device__ __forceinline__ Unit unit_scan(const Problem &P, const RowInfo &ri, const int32_t *irow, int first, int n,
                                           int lane) {
     Unit u{0, 0};
-    if (ri.pos >= ri.len_k || !row_ok(P, ri)) return u;   // behind the last sequence, or a bad row
+    if (ri.pos >= ri.len_k || P.total_k == 0 || !row_ok(P, ri)) return u;   // behind the last sequence, or a bad row
     int last = -1;
     irow += first;                                        // a multiple of 256 slots
     if ((P.topk & 3) == 0) {
@@ -416,7 +416,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         struct Ctx {                                         // a unit as its gathers see it
             RowInfo ri;
             const int32_t *irow;                             // its slots and how many there are
-            int left, fb;
+            int left, fb;                                    // fb: the cache row that stands in for masked slots
         };
         bool ok = run;
         int away = lw;                                       // ring positions up to this warp's next one (mod 7)
@@ -433,7 +433,10 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 x.z = s0 + 2 < c.left ? __ldg(c.irow + s0 + 2) : -1;
                 x.w = s0 + 3 < c.left ? __ldg(c.irow + s0 + 3) : -1;
             }
-            auto row_of = [&](int e) { return key_row(P, c.ri, mla::pair_visible(e, c.ri) ? e : c.fb); };
+            auto row_of = [&](int e) {
+                const int row = mla::pair_visible(e, c.ri) ? key_row_checked(P, c.ri, e) : -1;
+                return row < 0 ? c.fb : row;
+            };
             const int r0 = row_of(x.x), r1 = row_of(x.y), r2 = row_of(x.z), r3 = row_of(x.w);
             bool okw = true;
             if (lane == 0) {
@@ -461,7 +464,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 cur.left = K - first;
                 const bool got = wait(unit_full(j & 1), (j >> 1) & 1);
                 nb = got ? unit_nb[j & 1] : 0;
-                cur.fb = got ? unit_fb[j & 1] : 0;
+                // (row 0 where even that key has no row: the token's result then depends on it)
+                cur.fb = got && nb > 0 ? max(key_row_checked(P, cur.ri, unit_fb[j & 1]), 0) : 0;
                 ok = __all_sync(0xffffffffu, got);
                 if (ok && lane == 0) mbar_arrive(unit_free(j & 1));
                 b = 0;
@@ -783,9 +787,14 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             int e_own = entry(s_own), e_oth = entry(s_oth);
             int er = C::ER_MIN;
             for (int b = 0; b < nblocks; ++b, ++gb) {
-                const bool v_own = mla::pair_visible(e_own, ri), v_oth = mla::pair_visible(e_oth, ri);
-                const uint32_t c_own = v_own ? __ldg(kv_scale + key_row(P, ri, e_own)) : 0u;
-                const uint32_t c_oth = v_oth ? __ldg(kv_scale + key_row(P, ri, e_oth)) : 0u;
+                // a visible key without a row (a page outside the pool) is masked
+                const bool s_vis = mla::pair_visible(e_own, ri);
+                const int r_own = s_vis ? key_row_checked(P, ri, e_own) : -1;
+                const int r_oth = mla::pair_visible(e_oth, ri) ? key_row_checked(P, ri, e_oth) : -1;
+                const bool v_own = r_own >= 0, v_oth = r_oth >= 0;
+                if (s_vis && !v_own) raise_error(ERR_BOUNDS);
+                const uint32_t c_own = v_own ? __ldg(kv_scale + r_own) : 0u;
+                const uint32_t c_oth = v_oth ? __ldg(kv_scale + r_oth) : 0u;
                 if (b + 1 < nblocks) {
                     e_own = entry(s_own + C::BLK * (b + 1));
                     e_oth = entry(s_oth + C::BLK * (b + 1));

@@ -116,6 +116,8 @@ typedef struct dsa_problem {
  * only because ReLU(a*x) = a*ReLU(x) for a > 0 (a non-positive fp32 scale gives
  * unspecified scores; they live in device memory, so the host cannot check them; ue8m0
  * scales are positive by construction, 0xFF is NaN).
+ * A key whose block-table entry is no page of the pool (outside 0 .. S / 64 - 1) scores 0, and
+ * with e4m3 keys dsa_check_device_errors returns DSA_ERR_DEVICE_BOUNDS.
  */
 dsa_status_t dsa_indexer_scores(const dsa_problem_t *p, const void *q_idx, const void *q_scale,
                                 const void *k_idx, const void *k_scale, const float *w,
@@ -402,7 +404,9 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
  * negative, in the future or out of range, for repeated indices and for rows without a valid
  * slot (out = 0, lse = -inf).  Query rows behind the last sequence (t >= cu_q[B]) count as
  * rows without a valid slot.  What a masked slot's cache row holds (NaN included) has no
- * effect.
+ * effect.  A visible key whose block-table entry is no page of the pool (outside 0 .. S / 64 - 1)
+ * is masked, and dsa_check_device_errors returns DSA_ERR_DEVICE_BOUNDS; a token with no other
+ * visible key may get NaN.
  * Accuracy: q and the probabilities enter the tensor cores as two 8-bit floats each.  q's
  * elements are exact down to 2^-13 of their head's largest (the RoPE dims counted 16 times) and
  * off by at most 2^-21 of it below.  Products are exact and sums are fp32.  A key's weight
