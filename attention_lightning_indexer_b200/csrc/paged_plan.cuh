@@ -155,14 +155,13 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(Args a) {
             const int pg = pos >> 6;
             const int fresh = pg - (int)pages_of(s_c[lo]);
             int32_t *entry = a.block_table + (int64_t)lo * a.max_pages + pg;
-            int page;
-            if (fresh >= 0) {
-                page = __ldg(a.free_pages + head + s_pg[lo] + fresh);
-                if ((pos & 63) == 0) *entry = page;   // the page's first token
-            } else {
-                page = *entry;                         // cached pages are not written by this launch
-            }
-            if (page >= 0 && page < a.n_pages) row = page * 64 + (pos & 63);
+            // (cached pages are not written by this launch)
+            const int page = fresh >= 0 ? __ldg(a.free_pages + head + s_pg[lo] + fresh) : *entry;
+            const bool real = page >= 0 && page < a.n_pages;
+            // the page's first token stores it; -1 for one outside the pool, so that later steps reach
+            // neither that number nor what the entry held before
+            if (fresh >= 0 && (pos & 63) == 0) *entry = real ? page : -1;
+            if (real) row = page * 64 + (pos & 63);
             else raise_error(ERR_BOUNDS);
         }
         a.positions[t] = pos;

@@ -310,7 +310,8 @@ dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void
  * length.  With any of them the step is an empty batch: cu_q = cu_k = 0, every position 0
  * and row -1, counts[0..2] = 0, and block_table is left as it was.
  * A page number outside 0 .. n_pages - 1 (in block_table or free_pages) gives its tokens row
- * -1 and DSA_ERR_DEVICE_BOUNDS from dsa_check_device_errors.
+ * -1 and DSA_ERR_DEVICE_BOUNDS from dsa_check_device_errors; the rest of the step is planned as
+ * usual, and one from free_pages enters block_table as -1 (no page).
  *   1 <= batch <= 8192, n_tokens >= 0, max_pages >= 1, n_free >= 0, 1 <= n_pages < 2^25
  *   len_cached, len_new : [batch] int32   free_pages : [n_free] int32 (NULL if n_free == 0)
  * No array may overlap another.

@@ -1,4 +1,4 @@
-"""Block tables that name pages outside the pool: nothing is read or written
+"""Block tables and free lists that name pages outside the pool: nothing is read or written
 outside the caches, the error is reported, and the other sequences' results do not change."""
 from __future__ import annotations
 
@@ -118,3 +118,27 @@ def test_indexer_scores_keys_on_pages_outside_the_pool_zero(form, bad):
     want[0, 64:128] = 0
     want[1, 128:130] = 0
     assert torch.equal(got[0], want)
+
+
+@pytest.mark.parametrize("bad", BAD)
+def test_plan_stores_no_page_outside_the_pool(bad):
+    B, n_pages = 2, 12
+    cached, new = dev([10, 60], torch.int32), dev([60, 140], torch.int32)
+    table = dev([[3, 7, 9, 9], [4, 7, 9, 9]], torch.int32)        # stale numbers behind the cached pages
+    free = dev([5, bad, 6, 8], torch.int32)
+    z = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    cu_q, cu_k, pos, rows, counts = z(B + 1), z(B + 1), z(200), z(200), z(4)
+    dsa.dsa_paged_plan(cached, new, table, free, cu_q, cu_k, pos, rows, counts, n_pages=n_pages)
+    _expect_bounds()
+    # request 0 takes page 5; request 1 takes the bad number, 6 and 8
+    assert table.cpu().tolist() == [[3, 5, 9, 9], [4, -1, 6, 8]]
+    r = rows.cpu().numpy()
+    want = np.concatenate([3 * 64 + np.arange(10, 64), 5 * 64 + np.arange(6), 4 * 64 + np.arange(60, 64), np.full(64, -1),
+                           6 * 64 + np.arange(64), 8 * 64 + np.arange(8)])
+    np.testing.assert_array_equal(r, want)
+    assert counts.cpu().tolist() == [200, 4, 200, 0]
+    # the next step: a token on the page that has none gets no row
+    cached, new = dev([70, 110], torch.int32), dev([0, 1], torch.int32)
+    dsa.dsa_paged_plan(cached, new, table, free, cu_q, cu_k, pos[:1], rows[:1], counts, n_pages=n_pages, free_head=dev([4], torch.int32))
+    _expect_bounds()
+    assert rows[0].item() == -1 and pos[0].item() == 110
