@@ -48,7 +48,9 @@ EXPORTED = (
     "dsa_forward_noalloc_scratch_bytes",
     "dsa_check_device_errors",
     "dsa_cache_write",
+    "dsa_cache_write_bounded",
     "dsa_cache_write_fp8",
+    "dsa_cache_write_fp8_bounded",
     "dsa_paged_plan",
     "dsa_rope",
     "dsa_rope_frequencies",
@@ -147,7 +149,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.dsa_check_device_errors.argtypes = [P]
     lib.dsa_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
     lib.dsa_cache_write.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P]
+    lib.dsa_cache_write_bounded.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, i32, P]
     lib.dsa_cache_write_fp8.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, ctypes.c_int, P, P, P, P, P]
+    lib.dsa_cache_write_fp8_bounded.argtypes = [i32, P, P, P, P, P, P, P, P, ctypes.c_float, ctypes.c_int, P, P, P, P, i32, P]
     lib.dsa_paged_plan.argtypes = [i32, P, P, P, i32, P, i32, P, i32, P, P, P, P, i32, P, P]
     lib.dsa_rope.argtypes = [ctypes.POINTER(DsaRope), P, P, P, P, P]
     dbl = ctypes.c_double
@@ -163,6 +167,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     for name in ("dsa_indexer_scores", "dsa_topk", "dsa_indexer_topk_streaming", "dsa_sparse_mla_fwd", "dsa_dense_mla_fwd", "dsa_forward",
                  "dsa_forward_noalloc",
                  "dsa_check_device_errors", "dsa_selftest_bounded_wait", "dsa_cache_write", "dsa_cache_write_fp8",
+                 "dsa_cache_write_bounded", "dsa_cache_write_fp8_bounded",
                  "dsa_paged_plan", "dsa_rope", "dsa_rope_frequencies", "dsa_sparse_mla_fp8_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -304,13 +309,18 @@ def dsa_check_device_errors(stream=None) -> None:
     _check(load().dsa_check_device_errors(_stream(stream)), "dsa_check_device_errors")
 
 
+_MOST_ROWS = 2 ** 31 - 1
+
+
 def dsa_cache_write(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache,
                     kv_cache, eps: float = 1e-6, stream=None) -> None:
-    """Indexer-key and latent cache rows of new tokens (norms + RoPE; see include/dsa.h)."""
+    """Indexer-key and latent cache rows of new tokens (norms + RoPE; see include/dsa.h).  Rows past
+    the end of either cache are passed over and reported by dsa_check_device_errors."""
     lib = load()
-    _check(lib.dsa_cache_write(int(positions.numel()), _ptr(k_idx_raw), _ptr(kv_raw), _ptr(positions), _ptr(rows),
-                               _ptr(k_norm_w), _ptr(k_norm_b), _ptr(kv_norm_w), _ptr(inv_freq), eps,
-                               _ptr(k_idx_cache), _ptr(kv_cache), _stream(stream)), "dsa_cache_write")
+    n_rows = min(k_idx_cache.numel() // 128, kv_cache.numel() // 576, _MOST_ROWS)
+    _check(lib.dsa_cache_write_bounded(int(positions.numel()), _ptr(k_idx_raw), _ptr(kv_raw), _ptr(positions), _ptr(rows),
+                                       _ptr(k_norm_w), _ptr(k_norm_b), _ptr(kv_norm_w), _ptr(inv_freq), eps,
+                                       _ptr(k_idx_cache), _ptr(kv_cache), n_rows, _stream(stream)), "dsa_cache_write")
 
 
 def _need(ok: bool, what: str) -> None:
@@ -403,7 +413,8 @@ def dsa_cache_write_fp8(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, 
                         k_scale_cache, kv_cache, kv_scale_cache, idx_dtype: int = DSA_E4M3_UE8M0, eps: float = 1e-6,
                         stream=None) -> None:
     """dsa_cache_write into an 8-bit cache: the indexer key as ``idx_dtype`` says, the latent as
-    640 e4m3 codes and one ue8m0 scale per row (see include/dsa.h)."""
+    640 e4m3 codes and one ue8m0 scale per row (see include/dsa.h).  Rows past the end of either
+    cache are passed over and reported by dsa_check_device_errors."""
     n = positions.numel()
     key, scale = _KEY_TYPES.get(idx_dtype, (None, None))
     _need(key is not None, "dsa_cache_write_fp8: idx_dtype must be DSA_BF16, DSA_E4M3 or DSA_E4M3_UE8M0")
@@ -418,8 +429,9 @@ def dsa_cache_write_fp8(k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, 
     _need(k_idx_cache.shape[-1] == 128 and kv_cache.shape[-1] == 640
           and kv_scale_cache.numel() * 640 == kv_cache.numel()
           and (scale is None or k_scale_cache.numel() * 128 == k_idx_cache.numel()), "dsa_cache_write_fp8: cache shapes")
-    _check(load().dsa_cache_write_fp8(n, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], eps, idx_dtype, a[8], a[9], a[10],
-                                      a[11], _raw_stream(stream)), "dsa_cache_write_fp8")
+    n_rows = min(k_idx_cache.numel() // 128, kv_scale_cache.numel(), _MOST_ROWS)
+    _check(load().dsa_cache_write_fp8_bounded(n, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], eps, idx_dtype, a[8], a[9],
+                                              a[10], a[11], n_rows, _raw_stream(stream)), "dsa_cache_write_fp8")
 
 
 def dsa_sparse_mla_fp8_workspace_size(p: DsaProblem) -> int:

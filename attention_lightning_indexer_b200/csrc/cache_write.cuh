@@ -33,18 +33,26 @@ __device__ __forceinline__ void rot_cs(int pos, float inv_freq, float &c, float 
     s = (float)sd;
 }
 
+// Whether a token is written: not for a negative row (padding), nor for one past the caches' end,
+// which is reported.
+__device__ __forceinline__ bool row_in_cache(int64_t row, int n_rows, int lane) {
+    if (row >= 0 && row < n_rows) return true;
+    if (row >= 0 && lane == 0) raise_error(ERR_BOUNDS);
+    return false;
+}
+
 __global__ void __launch_bounds__(32 * WARPS)
 cache_write_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __nv_bfloat16 *__restrict__ kv_raw,
                    const int32_t *__restrict__ pos, const int32_t *__restrict__ rows,
                    const float *__restrict__ ln_w, const float *__restrict__ ln_b, const float *__restrict__ rms_w,
                    const float *__restrict__ inv_freq, float eps, __nv_bfloat16 *__restrict__ k_cache,
-                   __nv_bfloat16 *__restrict__ kv_cache) {
+                   __nv_bfloat16 *__restrict__ kv_cache, int n_rows) {
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * WARPS + (threadIdx.x >> 5);
     if (t >= n) return;                                       // whole warp
     const int p = __ldg(pos + t);
     const int64_t row = __ldg(rows + t);
-    if (row < 0) return;                                      // a token without a row (padding)
+    if (!row_in_cache(row, n_rows, lane)) return;
     // the 32 rotation angles of this position, pair i by lane i (both RoPEs use the same
     // frequencies); lanes read the ones they need by shuffles
     float c_lane, s_lane;

@@ -84,7 +84,7 @@ cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __n
                        const float *__restrict__ ln_w, const float *__restrict__ ln_b,
                        const float *__restrict__ rms_w, const float *__restrict__ inv_freq, float eps,
                        unsigned char *__restrict__ k_cache, void *__restrict__ k_scale,
-                       unsigned char *__restrict__ kv_cache, unsigned char *__restrict__ kv_scale) {
+                       unsigned char *__restrict__ kv_cache, unsigned char *__restrict__ kv_scale, int n_rows) {
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * FP8_WARPS + (threadIdx.x >> 5);
     if (t >= n) return;                                       // whole warp
@@ -102,7 +102,7 @@ cache_write_fp8_kernel(int n, const __nv_bfloat16 *__restrict__ k_raw, const __n
     const uint32_t zr = __ldg(reinterpret_cast<const uint32_t *>(src + 128) + lane);
     double sn, cs;
     sincos((double)p * (double)__ldg(inv_freq + lane), &sn, &cs);
-    if (row < 0) return;                                      // a token without a row (padding)
+    if (!row_in_cache(row, n_rows, lane)) return;
     float x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = __uint_as_float((uint32_t)xr[j] << 16);

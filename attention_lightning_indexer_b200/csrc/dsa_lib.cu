@@ -710,7 +710,15 @@ dsa_status_t dsa_indexer_topk_streaming(const dsa_problem_t *p, const void *q_id
 dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw, const int32_t *positions,
                              const int32_t *rows, const float *k_norm_w, const float *k_norm_b, const float *kv_norm_w,
                              const float *inv_freq, float eps, void *k_idx_cache, void *kv_cache, dsa_stream_t stream) {
-    if (n_tokens < 0 || !(eps >= 0.0f)) return DSA_ERR_INVALID_ARG;
+    return dsa_cache_write_bounded(n_tokens, k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq,
+                                   eps, k_idx_cache, kv_cache, INT32_MAX, stream);
+}
+
+dsa_status_t dsa_cache_write_bounded(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw, const int32_t *positions,
+                                     const int32_t *rows, const float *k_norm_w, const float *k_norm_b,
+                                     const float *kv_norm_w, const float *inv_freq, float eps, void *k_idx_cache,
+                                     void *kv_cache, int32_t n_rows, dsa_stream_t stream) {
+    if (n_tokens < 0 || !(eps >= 0.0f) || n_rows < 0) return DSA_ERR_INVALID_ARG;
     if (n_tokens == 0) return DSA_OK;
     const void *ptrs[] = {k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache, kv_cache};
     for (const void *q : ptrs)
@@ -719,7 +727,7 @@ dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void
     dsa::cache::cache_write_kernel<<<grid, 32 * dsa::cache::WARPS, 0, (cudaStream_t)stream>>>(
         n_tokens, reinterpret_cast<const __nv_bfloat16 *>(k_idx_raw), reinterpret_cast<const __nv_bfloat16 *>(kv_raw),
         positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, eps, reinterpret_cast<__nv_bfloat16 *>(k_idx_cache),
-        reinterpret_cast<__nv_bfloat16 *>(kv_cache));
+        reinterpret_cast<__nv_bfloat16 *>(kv_cache), n_rows);
     return launch_status();
 }
 
@@ -728,7 +736,17 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
                                  const float *kv_norm_w, const float *inv_freq, float eps, dsa_dtype_t idx_dtype,
                                  void *k_idx_cache, void *k_scale_cache, void *kv_cache, void *kv_scale_cache,
                                  dsa_stream_t stream) {
-    if (n_tokens < 0 || !(eps >= 0.0f) || isinf(eps)) return DSA_ERR_INVALID_ARG;
+    return dsa_cache_write_fp8_bounded(n_tokens, k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w,
+                                       inv_freq, eps, idx_dtype, k_idx_cache, k_scale_cache, kv_cache, kv_scale_cache,
+                                       INT32_MAX, stream);
+}
+
+dsa_status_t dsa_cache_write_fp8_bounded(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw,
+                                         const int32_t *positions, const int32_t *rows, const float *k_norm_w,
+                                         const float *k_norm_b, const float *kv_norm_w, const float *inv_freq, float eps,
+                                         dsa_dtype_t idx_dtype, void *k_idx_cache, void *k_scale_cache, void *kv_cache,
+                                         void *kv_scale_cache, int32_t n_rows, dsa_stream_t stream) {
+    if (n_tokens < 0 || !(eps >= 0.0f) || isinf(eps) || n_rows < 0) return DSA_ERR_INVALID_ARG;
     if (idx_dtype != DSA_BF16 && idx_dtype != DSA_E4M3 && idx_dtype != DSA_E4M3_UE8M0) return DSA_ERR_UNSUPPORTED;
     if (n_tokens == 0) return DSA_OK;
     const void *ptrs[] = {k_idx_raw, kv_raw, positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, k_idx_cache, kv_cache};
@@ -741,7 +759,7 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
         kernel<<<grid, 32 * dsa::cache::FP8_WARPS, 0, (cudaStream_t)stream>>>(
             n_tokens, reinterpret_cast<const __nv_bfloat16 *>(k_idx_raw), reinterpret_cast<const __nv_bfloat16 *>(kv_raw),
             positions, rows, k_norm_w, k_norm_b, kv_norm_w, inv_freq, eps, static_cast<unsigned char *>(k_idx_cache),
-            k_scale_cache, static_cast<unsigned char *>(kv_cache), static_cast<unsigned char *>(kv_scale_cache));
+            k_scale_cache, static_cast<unsigned char *>(kv_cache), static_cast<unsigned char *>(kv_scale_cache), n_rows);
     };
     if (idx_dtype == DSA_BF16) launch(dsa::cache::cache_write_fp8_kernel<dsa::cache::KEY_BF16>);
     else if (idx_dtype == DSA_E4M3) launch(dsa::cache::cache_write_fp8_kernel<dsa::cache::KEY_E4M3>);

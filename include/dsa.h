@@ -288,6 +288,17 @@ dsa_status_t dsa_cache_write(int32_t n_tokens, const void *k_idx_raw, const void
                              float eps, void *k_idx_cache, void *kv_cache, dsa_stream_t stream);
 
 /*
+ * dsa_cache_write into caches of n_rows rows: a token with rows[t] >= n_rows is passed over as
+ * well, and dsa_check_device_errors returns DSA_ERR_DEVICE_BOUNDS.  (dsa_cache_write does not know
+ * where its caches end and writes where rows[t] says.)
+ */
+dsa_status_t dsa_cache_write_bounded(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw,
+                                     const int32_t *positions, const int32_t *rows, const float *k_norm_w,
+                                     const float *k_norm_b, const float *kv_norm_w, const float *inv_freq,
+                                     float eps, void *k_idx_cache, void *kv_cache, int32_t n_rows,
+                                     dsa_stream_t stream);
+
+/*
  * Page plan of one step: sequence offsets, slot map and block-table entries from the
  * requests' lengths, made on the GPU (paged caches of 64-token pages, "DeepSeek-V3.2" (miles
  * docs) §5.3; the pages give the page size, the bookkeeping is this build's).  Request b holds
@@ -398,6 +409,14 @@ dsa_status_t dsa_cache_write_fp8(int32_t n_tokens, const void *k_idx_raw, const 
                                  const float *k_norm_b, const float *kv_norm_w, const float *inv_freq,
                                  float eps, dsa_dtype_t idx_dtype, void *k_idx_cache, void *k_scale_cache,
                                  void *kv_cache, void *kv_scale_cache, dsa_stream_t stream);
+
+/* dsa_cache_write_fp8 into caches of n_rows rows, as dsa_cache_write_bounded. */
+dsa_status_t dsa_cache_write_fp8_bounded(int32_t n_tokens, const void *k_idx_raw, const void *kv_raw,
+                                         const int32_t *positions, const int32_t *rows, const float *k_norm_w,
+                                         const float *k_norm_b, const float *kv_norm_w, const float *inv_freq,
+                                         float eps, dsa_dtype_t idx_dtype, void *k_idx_cache,
+                                         void *k_scale_cache, void *kv_cache, void *kv_scale_cache,
+                                         int32_t n_rows, dsa_stream_t stream);
 
 /*
  * dsa_sparse_mla_fwd over the 8-bit latent cache of dsa_cache_write_fp8: the same z, out and
