@@ -1008,6 +1008,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         tmem_st16(oa + 16 * c, o);
                     }
                     tmem_wait_st();
+                    // before the st.async below too: their bytes on p_in are all that the next PV waits for
+                    // from the warps whose P' goes to the other CTA
+                    tc_fence_before();
                 }
                 er = er_new;
                 // ---- P'^T of this thread's key for its 64 heads, 16 heads at a time
