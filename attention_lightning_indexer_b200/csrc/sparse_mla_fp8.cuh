@@ -175,7 +175,8 @@ __device__ __forceinline__ void split_8bit(__half2 x, uint32_t &hi, uint32_t &lo
 }
 
 // Bounded waits (a try that fails has suspended the warp for 1.5 us, measured: 0.2 s in all) that
-// raise no error: the role that gives up does, when it stops the pair.  The 60 waits of the kernel with the clock and
+// raise no error: the role that gives up stops the pair by its flag, and the teardown of a pair
+// that was stopped raises it and makes the pair's rows NaN.  The 60 waits of the kernel with the clock and
 // the error flag at each of them were enough code to miss in the instruction caches (583 us
 // instead of 556 for 1024 queries).
 constexpr int WAIT_TRIES = 1 << 17;
@@ -224,6 +225,28 @@ __device__ __forceinline__ Unit unit_scan(const Problem &P, const RowInfo &ri, c
     u.nblocks = (last + Cfg::BLK) / Cfg::BLK;
     u.fallback = __ldg(irow + last);
     return u;
+}
+
+// 256 threads (st) fill CTA cr's part of a unit's output (2 x 128 dims of every head, the lse of 64
+// heads) with one value each.
+template <bool SPLIT>
+__device__ __forceinline__ void fill_unit(const mla::SplitArgs &sp, __nv_bfloat16 *out, float *lse, int t, int split, int cr,
+                                          int st, float o, float l) {
+    const int64_t base = SPLIT ? ((int64_t)t * sp.nsplit + split) * 128 : (int64_t)t * 128;   // rows of 512
+    const uint32_t w = sm100::pack_bf16x2(o, o);
+#pragma unroll 1
+    for (int e = st; e < 128 * 32; e += 256) {
+        const int h = e >> 5, part = e & 31;                 // 32 x 8 dims per head
+        const int64_t at = (base + h) * 512 + 256 * (part >> 4) + 128 * cr + 8 * (part & 15);
+        if (SPLIT) {
+            float4 *op = reinterpret_cast<float4 *>(sp.o_part + at);
+            op[0] = make_float4(o, o, o, o);
+            op[1] = make_float4(o, o, o, o);
+        } else {
+            *reinterpret_cast<uint4 *>(out + at) = make_uint4(w, w, w, w);
+        }
+    }
+    if (st < 128 && (st >> 6) == cr) (SPLIT ? sp.lse_part : lse)[base + st] = l;
 }
 
 template <bool SPLIT>
@@ -866,6 +889,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int nblocks = got ? unit_nb[j & 1] : 0;
             if (named_bar_or(1, 256, !got || misc[1] != 0)) {
                 ok = false;
+                if (st == 0) abort_pair();
                 break;
             }
             if (j == 0 && nblocks > 0) {                     // what the preparing warps do for later units
@@ -1068,9 +1092,8 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
             if (!ok && st == 0) abort_pair();
 
-            // ---- row sums of the pair: lse, and the output factors for the epilogue
-            const int64_t obase = (int64_t)t * 128;
-            const int64_t pbase = ((int64_t)t * nsplit + split) * 128;   // partial rows (split mode)
+            // ---- row sums of the pair: lse, and the output factors for the epilogue (after an abort the
+            // teardown writes the rows)
             if (nblocks > 0 && ok) {
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
@@ -1087,40 +1110,23 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                                  mapa_shared(lbar, (uint32_t)peer));
                     if (st == 0) mbar_expect_tx(lbar, 128 * 4);
                     const bool okl = wait_cluster(lbar, nq & 1);
+                    if (!okl) misc[1] = 1;
                     // the two CTAs add the same two numbers in the same order
                     const float l_tot = cr == 0 ? l_cta + xl[h] : xl[h] + l_cta;
                     // O^T holds sum p 2^(e - er + BASE) code
                     fo[128 * (nq & 1) + h] =
                         !okl ? NAN : (l_tot != 0.f ? ue8m0_to_float((uint32_t)(er - C::BASE)) / l_tot : 0.f);
                     if ((h >> 6) == cr) {
+                        const int64_t at = SPLIT ? ((int64_t)t * nsplit + split) * 128 + h : (int64_t)t * 128 + h;
                         const float lv =
                             okl ? (l_tot != 0.f ? (log2f(l_tot) - mq[mqh]) * 0.6931471805599453f : -INFINITY) : NAN;
-                        if (SPLIT) sp.lse_part[pbase + h] = lv;
-                        else lse[obase + h] = lv;
+                        (SPLIT ? sp.lse_part : lse)[at] = lv;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(fo_full(nq & 1));
                 }
             } else {
-                // no visible slot: out = 0, lse = -inf (an aborted pipeline: NaN)
-                const uint32_t fill = nblocks == 0 ? 0u : 0x7fc07fc0u;
-                for (int e = st; e < 128 * 32; e += 256) {
-                    const int h = e >> 5, part = e & 31;      // 32 x 16 bytes per head: the CTA's 2 x 128 dims
-                    const int d0 = 256 * (part >> 4) + 128 * cr + 8 * (part & 15);
-                    if (SPLIT) {
-                        const float f = __uint_as_float(nblocks == 0 ? 0u : 0x7fc00000u);
-                        float4 *op = reinterpret_cast<float4 *>(sp.o_part + (pbase + h) * 512 + d0);
-                        op[0] = make_float4(f, f, f, f);
-                        op[1] = make_float4(f, f, f, f);
-                    } else {
-                        *reinterpret_cast<uint4 *>(out + (obase + h) * 512 + d0) = make_uint4(fill, fill, fill, fill);
-                    }
-                }
-                if (st < 128 && (st >> 6) == cr) {
-                    const float lv = nblocks == 0 ? -INFINITY : NAN;
-                    if (SPLIT) sp.lse_part[pbase + st] = lv;
-                    else lse[obase + st] = lv;
-                }
+                fill_unit<SPLIT>(sp, out, lse, t, split, cr, st, 0.f, -INFINITY);   // no visible slot
             }
             gb0 += nblocks;
             if (nblocks > 0) {
@@ -1149,6 +1155,15 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (pmax >= 0) wait_cluster(pfull(tid), (uint32_t)(pmax / C::NSLOT) & 1u);
         }
         cluster_sync();
+        // A wait that gave up may have left any of this pair's rows unwritten or wrong: all of them are NaN.
+        if (tid == 0) raise_error(ERR_WAIT_TIMEOUT);
+        int block, st;                                       // (read again: kept all along they cost spills)
+        asm volatile("mov.u32 %0, %%ctaid.x;\n\tmov.u32 %1, %%tid.x;" : "=r"(block), "=r"(st));
+        st -= 32 * C::SOFT0;
+        const int parts = SPLIT ? sp.nsplit : 1;
+        if (st >= 0)
+            for (int u = block >> 1; u < P.total_q * parts; u += (int)(gridDim.x >> 1))
+                fill_unit<SPLIT>(sp, out, lse, P.total_q - 1 - u / parts, u % parts, block & 1, st, NAN, NAN);
     }
     if (warp == 0) {
         tc_fence_after();

@@ -437,6 +437,8 @@ dsa_status_t dsa_cache_write_fp8_bounded(int32_t n_tokens, const void *k_idx_raw
  * So light keys beside a heavy one lose bits only if they share its block.  A block whose heaviest
  * key is below 2^-20 of the heaviest so far is held relative to 2^-20 of that one, and a scale
  * that is below 2^-24 of the row's largest so far counts as 2^-24 of it here.
+ * If a bounded wait gives up (DSA_ERR_DEVICE_TIMEOUT from dsa_check_device_errors), out and lse of
+ * every row that its pair of SMs had a part of are NaN.
  *   kv : uint8 [S, 640]   kv_scale : uint8 [S] ue8m0   other tensors as dsa_sparse_mla_fwd
  *   workspace : device, >= dsa_sparse_mla_fp8_workspace_size(p) bytes, 256-byte aligned (may
  *               be NULL when that is 0; at most 31 MB, 11 from 38 query rows on).  It holds the
