@@ -385,8 +385,8 @@ dsa_status_t mla_fp8_launch(const dsa_problem_t *p, const void *q, const void *k
     return launch_status();
 }
 
-// One CTA waits on an mbarrier that nothing arrives at, so its bounded wait runs out
-// after `limit_ns`: exercises the give-up path (error flag, no hang) with no copy or MMA
+// One CTA waits on an mbarrier that nothing arrives at, so its bounded waits (both forms, one
+// after the other) run out after `limit_ns` each: exercises the give-up path (error flag, no hang) with no copy or MMA
 // in flight.
 __global__ void bounded_wait_selftest_kernel(uint64_t limit_ns) {
     using namespace dsa::sm100;
@@ -396,6 +396,9 @@ __global__ void bounded_wait_selftest_kernel(uint64_t limit_ns) {
         mbar_init(b, 1);
         fence_barrier_init();
         mbar_wait_for(b, 0, limit_ns);
+        // the other form (its error is its caller's): neither success nor an early end
+        const uint64_t t0 = globaltimer();
+        if (dsa::mla8::wait(b, 0, (uint32_t)limit_ns) || globaltimer() - t0 < limit_ns) dsa::raise_error(dsa::ERR_BOUNDS);
     }
 }
 

@@ -29,6 +29,13 @@ __device__ __forceinline__ uint64_t globaltimer() {
     return t;
 }
 
+// Its lower half: enough for spans below 4 s.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

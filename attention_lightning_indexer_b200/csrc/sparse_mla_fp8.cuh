@@ -174,23 +174,30 @@ __device__ __forceinline__ void split_8bit(__half2 x, uint32_t &hi, uint32_t &lo
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E5M2);
 }
 
-// Bounded waits (a try that fails has suspended the warp for 1.5 us, measured: 0.2 s in all) that
-// raise no error: the role that gives up stops the pair by its flag, and the teardown of a pair
-// that was stopped raises it and makes the pair's rows NaN.  The 60 waits of the kernel with the clock and
-// the error flag at each of them were enough code to miss in the instruction caches (583 us
-// instead of 556 for 1024 queries).
-constexpr int WAIT_TRIES = 1 << 17;
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+// Bounded waits of 0.2 s that raise no error: the role that gives up stops the pair by its flag, and
+// the teardown of a pair that was stopped raises it and makes the pair's rows NaN.  The clock is
+// read once in 4096 tries (how long a failed try suspends the warp is not specified; 1.5 us here):
+// the 60 waits of the kernel with the clock and the error flag at each try were enough code to
+// miss in the instruction caches (583 us instead of 556 for 1024 queries).
+constexpr uint32_t WAIT_NS = 200000000u, WAIT_STRIDE = 4096u;
+template <typename Try>
+__device__ __forceinline__ bool wait_until(Try tried, uint32_t limit_ns) {
+    uint32_t start = 0;
 #pragma unroll 1
-    for (int i = 0; i < WAIT_TRIES; ++i)
-        if (sm100::mbar_try_wait(bar, parity)) return true;
-    return false;
+    for (uint32_t i = 1;; ++i) {
+        if (tried()) return true;
+        if ((i & (WAIT_STRIDE - 1u)) == 0u) {
+            const uint32_t now = sm100::globaltimer_lo();
+            if (i == WAIT_STRIDE) start = now;
+            else if (now - start > limit_ns) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t limit_ns = WAIT_NS) {
+    return wait_until([=] { return sm100::mbar_try_wait(bar, parity); }, limit_ns);
 }
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < WAIT_TRIES; ++i)
-        if (sm100::mbar_try_wait_cluster(bar, parity)) return true;
-    return false;
+    return wait_until([=] { return sm100::mbar_try_wait_cluster(bar, parity); }, WAIT_NS);
 }
 
 struct Unit {

@@ -454,8 +454,9 @@ dsa_status_t dsa_sparse_mla_fp8_fwd(const dsa_problem_t *p, const void *q, const
 
 /*
  * Self-test of the device-side failure path (no counterpart on the pages): launches one
- * CTA whose bounded wait on a barrier that nothing signals gives up after `limit_us`
- * microseconds (1 .. 10000), as a stalled pipeline wait would.  No copy or tensor-core
+ * CTA whose bounded waits (both forms that the kernels use, one after the other) on a barrier
+ * that nothing signals give up after `limit_us` microseconds (1 .. 10000; the second form up to 15
+ * ms later), as a stalled pipeline wait would.  No copy or tensor-core
  * operation is in flight.  The next dsa_check_device_errors() then returns
  * DSA_ERR_DEVICE_TIMEOUT and clears the flag; the device stays usable.
  */
