@@ -979,7 +979,7 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     const float m_blk = fmaxf(m_cta, okx ? xm[128 * (gb & 1) + h] : m_cta);
                     // the largest so far: what was seen before loses as much as the largest scale gained,
                     // SPAN at most (`sunk` so far)
-                    const float gain = b == 0 ? 0.f : fminf((float)(er_new - er), C::SPAN - sunk);
+                    const float gain = m_top == -INFINITY ? 0.f : fminf((float)(er_new - er), C::SPAN - sunk);
                     sunk += gain;
                     m_top = fmaxf(m_top - gain, m_blk);
                     // up where the block exceeds the reference by more than TAU, down where it lies more than
