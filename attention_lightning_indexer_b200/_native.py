@@ -398,7 +398,9 @@ def dsa_rope(x, positions, inv_freq, out, layout: int = DSA_ROPE_INTERLEAVED, ro
 def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: float = 4096.0,
                          beta_fast: float = 32.0, beta_slow: float = 1.0):
     """RoPE frequencies (a host fp32 tensor [rope_dim / 2]) and the attention factor; ``factor``
-    > 1 stretches them for long contexts (see include/dsa.h)."""
+    > 1 stretches them for long contexts.  The factor belongs on queries and keys both; the cache
+    writes do not scale keys, so a model that uses it gives its square as ``scale`` of dsa_rope
+    (see include/dsa.h)."""
     freq = torch.empty(max(rope_dim, 0) // 2, dtype=torch.float32)
     att = ctypes.c_double()
     _check(load().dsa_rope_frequencies(rope_dim, base, factor, original_len, beta_fast, beta_slow,

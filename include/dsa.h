@@ -344,7 +344,7 @@ typedef struct dsa_rope_desc {
     dsa_rope_dtype_t dtype;
     int64_t x_token_stride, x_head_stride;       /* in elements; the last dimension is dense */
     int64_t out_token_stride, out_head_stride;
-    float scale;                           /* multiplies the rotated dims (1, or an attention factor) */
+    float scale;                           /* multiplies the rotated dims (1, or see dsa_rope_frequencies) */
     int32_t transposed;                    /* nonzero: turn by the negative angle */
 } dsa_rope_desc_t;
 
@@ -374,7 +374,12 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t *r, const void *x, const int32_t *po
  * high = ceil(r(beta_slow)) clipped to <= rope_dim - 1 and w_i = clip((i - low) /
  * max(high - low, 0.001), 0, 1):   inv_freq[i] = base^(-2i / rope_dim) * (w_i / factor + 1 - w_i).
  *   inv_freq : host [rope_dim / 2] fp32
- *   attention_factor : host, may be NULL: 0.1 * ln(factor) + 1 for factor > 1, else 1
+ *   attention_factor : host, may be NULL: 0.1 * ln(factor) + 1 for factor > 1, else 1.  The rule
+ *           multiplies cosine and sine of queries AND keys by it, so the rotated dims' part of
+ *           every score by its square.  The cache writes leave keys unscaled: the queries take
+ *           the square, as dsa_rope's `scale` (the factor itself would be half of it).  A model that
+ *           puts it on whole scores instead takes scale 1 and sm_scale times the square; one
+ *           whose softmax scale is given without it (1/sqrt(192) here) uses neither.
  * DSA_ERR_INVALID_ARG for a NULL array, an odd or non-positive rope_dim, base <= 1,
  * factor < 1, original_len < 1 (with factor > 1), beta_fast < beta_slow or beta_slow <= 0.
  */
