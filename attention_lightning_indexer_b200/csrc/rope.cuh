@@ -10,8 +10,9 @@
 // HBM-bound: every rotated element is read and written once.  Angles, cosines and sines are
 // taken in fp64 (at position 163,840 an fp32 angle is off by 2^-7 rad) once per token and
 // pair, times scale rounded to fp32 in shared memory; the heads of the token share them.  A
-// CTA takes whole tokens: one each when there are few, several where that still leaves a full
-// grid, so that all its warps evaluate angles at once and then stream without another barrier.
+// CTA takes whole tokens: as many as give its threads about four items each, or two where tokens
+// have more than that and two still leave a full grid, so that all its warps evaluate angles at
+// once and then stream without another barrier.
 // A thread keeps its place within a head (one 16-byte vector, its pairs' cosines and sines in
 // registers) and goes from head to head by adding strides: placing each vector by divisions
 // cost more instructions (177 a vector) than rotating it.

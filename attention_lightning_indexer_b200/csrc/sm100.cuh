@@ -297,12 +297,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 namespace dsa {
 namespace sm100 {
 
-// Orders shared-memory data written through the generic proxy (cp.async copies whose
-// completion this thread has observed on an mbarrier) before this thread's following
-// async-proxy operations (tensor-core operand reads).
+// Orders global data written or read through the generic proxy before this thread's following
+// async-proxy operations on it (bulk copies), and so for the thread that waited for such a writer.
 __device__ __forceinline__ void fence_proxy_async_global() {
     asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+
+// Orders shared-memory data written through the generic proxy (cp.async copies whose
+// completion this thread has observed on an mbarrier) before this thread's following
+// async-proxy operations (tensor-core operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
