@@ -20,9 +20,9 @@
 // it conversions between the formats, which run at 8 cycles a warp instruction.
 // One warp per token; lane i owns RoPE pair i of both parts, so the angle it evaluates needs
 // no exchange.  1.4 KB read and 0.8 KB written per token: 10.9 us at 32768 tokens and the copy
-// bandwidth; measured 21.6 us, bound by issue (about 500 instructions a token, of them the fp64
+// bandwidth; measured 21.8 us, bound by issue (about 500 instructions a token, of them the fp64
 // sine and cosine 1.5 us) and by what a token's chain of loads, sums and roots leaves uncovered.
-// 64 tokens: 3.1 us.
+// 64 tokens: 3.0 us.
 #pragma once
 
 #include "cache_write.cuh"

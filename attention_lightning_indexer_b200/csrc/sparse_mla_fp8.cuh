@@ -57,16 +57,16 @@
 // 621 us with TAU = 2.8 and BASE = 6, 565 with 4.8 and 4 (both before DOWN); with DOWN = 4 they
 // take 566, with 6 555, without it 552 (scores of deviation 1.7, where it does little else).
 // DEPTH ends the way down (what is 2^-20 of the heaviest so far needs no more), and SPAN bounds e -
-// er from below, so that p and its sums stay below 2^60 whatever the scales.  The sum l takes p
+// er from below, so that p and its sums stay below 2^90 whatever the scales.  The sum l takes p
 // itself in fp32.
 //
-// Measured: 1024 queries x 2048 keys 566 us (tensor floor 354 us; the bf16 form 961 us), 64
-// queries 50 us (floor 22; bf16 85), one query over 8 pairs 18 us with the merge.  A block takes 4.2 us with 64
-// pairs at work and 4.7 with all 74 (tensor cores 3.2), of it the copy engine 3.5: 288 gather4 of
-// 512 bytes per CTA at 12 ns; and shared memory 6800 of 9050 cycles: tensor cores 3456
-// wavefronts, loads and stores 2100, gathers 1152.  The chain QK, maxima, their exchange, P', PV
-// has no slack beside those, and the SM clock falls to 1.73 GHz: leaving out any one of the
-// gathers for PV, half of the QK or PV MMAs, or the split of P' saved 4 %.
+// Measured (graph replays): 1024 queries x 2048 keys 565 to 580 us (tensor floor 354 us; the bf16
+// form 961 us), 64 queries 51 us (floor 22; bf16 85), one query over 8 pairs 18.5 us with the
+// merge.  A block takes 4.9 us with all 74 pairs at work (tensor cores 3.2), of it the copy engine
+// 3.5: 288 gather4 of 512 bytes per CTA at 12 ns; and shared memory 7400 of 9700 cycles: tensor
+// cores 3456 wavefronts, loads and stores 2790, gathers 1152.  The chain QK, maxima, their
+// exchange, P', PV has no slack beside those, and the SM clock falls to 1.73 GHz: leaving out any
+// one of the gathers for PV, half of the QK or PV MMAs, or the split of P' saved 4 %.
 //
 // Warp roles (20 warps): 0-6 gather (one ring slot each), 7 issues the MMAs (even CTA), 8-11
 // prepare (warp 8 also publishes each unit's block count; they split q into hi and lo, each head
