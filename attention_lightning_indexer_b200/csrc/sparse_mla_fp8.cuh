@@ -60,7 +60,7 @@
 // er from below, so that p and its sums stay below 2^90 whatever the scales.  The sum l takes p
 // itself in fp32.
 //
-// Measured (graph replays): 1024 queries x 2048 keys 565 to 580 us (tensor floor 354 us; the bf16
+// Measured (graph replays): 1024 queries x 2048 keys 565 to 590 us (tensor floor 354 us; the bf16
 // form 961 us), 64 queries 51 us (floor 22; bf16 85), one query over 8 pairs 18.5 us with the
 // merge.  A block takes 4.9 us with all 74 pairs at work (tensor cores 3.2), of it the copy engine
 // 3.5: 288 gather4 of 512 bytes per CTA at 12 ns; and shared memory 7400 of 9700 cycles: tensor
@@ -494,8 +494,16 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 cur.left = K - first;
                 const bool got = wait(unit_full(j & 1), (j >> 1) & 1);
                 nb = got ? unit_nb[j & 1] : 0;
-                // (row 0 where even that key has no row: the token's result then depends on it)
-                cur.fb = got && nb > 0 ? max(key_row_checked(P, cur.ri, unit_fb[j & 1]), 0) : 0;
+                cur.fb = got && nb > 0 ? key_row_checked(P, cur.ri, unit_fb[j & 1]) : 0;
+                if (cur.fb < 0) {                            // on a page outside the pool: any key that is not
+                    int other = 0;                           // (none: row 0, which the output leaves out)
+#pragma unroll 1
+                    for (int i = lane; i < min(cur.left, nb * C::BLK); i += 32) {
+                        const int e = __ldg(cur.irow + i);
+                        if (mla::pair_visible(e, cur.ri)) other = max(other, key_row_checked(P, cur.ri, e));
+                    }
+                    cur.fb = __reduce_max_sync(0xffffffffu, other);
+                }
                 ok = __all_sync(0xffffffffu, got);
                 if (ok && lane == 0) mbar_arrive(unit_free(j & 1));
                 b = 0;
@@ -690,6 +698,9 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (!__all_sync(0xffffffffu, fine)) return false;
             tc_fence_after();
             const float *f = fo + 128 * (pn & 1);
+            // no key had a row (its page was outside the pool), then for no head: zeros, whatever row 0 put
+            // into O^T
+            const bool none = f[0] == 0.f;
             // O^T block i: lanes = value dims 256 i + 128 cr + 32 pw + lane, columns = heads
             const bool odd = (lane & 1) != 0;
 #pragma unroll 1
@@ -698,6 +709,10 @@ sparse_mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 uint32_t o[32];
                 tmem_ld32(tmem + ((uint32_t)(pw * 32) << 16) + C::TMEM_O + 32 * c8, o);
                 tmem_wait_ld();
+                if (none) {
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) o[h] = 0u;
+                }
                 if (c8 == 7) {
                     tc_fence_before();
                     __syncwarp();

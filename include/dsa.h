@@ -430,8 +430,7 @@ dsa_status_t dsa_cache_write_fp8_bounded(int32_t n_tokens, const void *k_idx_raw
  * slot (out = 0, lse = -inf).  Query rows behind the last sequence (t >= cu_q[B]) count as
  * rows without a valid slot.  What a masked slot's cache row holds (NaN included) has no
  * effect.  A visible key whose block-table entry is no page of the pool (outside 0 .. S / 64 - 1)
- * is masked, and dsa_check_device_errors returns DSA_ERR_DEVICE_BOUNDS; a token with no other
- * visible key may get NaN.
+ * is masked, and dsa_check_device_errors returns DSA_ERR_DEVICE_BOUNDS.
  * Accuracy: q and the probabilities enter the tensor cores as two 8-bit floats each.  q's
  * elements are exact down to 2^-13 of their head's largest (the RoPE dims counted 16 times) and
  * off by at most 2^-21 of it below.  Products are exact and sums are fp32.  A key's weight

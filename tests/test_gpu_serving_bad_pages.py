@@ -35,25 +35,28 @@ def _problem(table, lens, topk, form, repeat):
 
 
 @pytest.mark.parametrize("repeat", [1, 30])
+@pytest.mark.parametrize("page", [1, 2])                     # a page of sequence 1: keys 64 .., or its last keys
 @pytest.mark.parametrize("bad", BAD)
-def test_attention_masks_keys_on_pages_outside_the_pool(bad, repeat):
+def test_attention_masks_keys_on_pages_outside_the_pool(bad, page, repeat):
     rng = np.random.default_rng(1)
     lens, topk = [200, 150, 700 - 64 * 3], 600
     good = np.full((3, 8), -1, np.int64)
     good[0, :4], good[1, :3], good[2, :7] = [0, 1, 2, 3], [4, 5, 6], [7, 8, 9, 10, 11, 0, 1]
     lens[2] = 448
     table = good.copy()
-    table[1, 1] = bad                        # keys 64 .. 127 of sequence 1
+    table[1, page] = bad
     codes, byte = ref.quantise_latent(rng.standard_normal((768, 512)), rng.standard_normal((768, 64)))
+    codes[0] = 0x7F                          # (key 0 of sequence 0 is NaN: listed by nobody below)
     T = 3 * repeat
     q = torch.randn(T, 128, 576, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
     seq = np.repeat(np.arange(3), repeat)
     idx = np.full((T, topk), -1, np.int32)
     for t in range(T):
         n = lens[seq[t]] - repeat + t % repeat + 1
-        idx[t, :n] = np.arange(n)
+        idx[t, 1:n] = np.arange(1, n)
+    idx[seq == 2] = np.where(idx[seq == 2] == 320, -1, idx[seq == 2])   # (its key 320 is the same row)
     outs = []
-    for tab, ix in ((table, idx), (good, np.where((seq == 1)[:, None] & (idx >= 64) & (idx < 128), -1, idx))):
+    for tab, ix in ((table, idx), (good, np.where((seq == 1)[:, None] & (idx // 64 == page), -1, idx))):
         p = _problem(tab, lens, topk, dsa.DSA_BF16, repeat)
         out, lse = torch.zeros(T, 128, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(T, 128, device=DEV)
         ws = torch.zeros(max(256, dsa.dsa_sparse_mla_fp8_workspace_size(p)), dtype=torch.uint8, device=DEV)
@@ -67,23 +70,51 @@ def test_attention_masks_keys_on_pages_outside_the_pool(bad, repeat):
     assert torch.isfinite(outs[0][1]).all()
 
 
+@pytest.mark.parametrize("topk", [128, 600])
 @pytest.mark.parametrize("bad", BAD)
-def test_attention_of_a_token_whose_pages_are_all_bad_changes_no_other(bad):
+def test_attention_of_a_token_whose_pages_are_all_bad_changes_no_other(bad, topk):
     rng = np.random.default_rng(2)
     codes, byte = ref.quantise_latent(rng.standard_normal((768, 512)), rng.standard_normal((768, 64)))
+    codes[0], byte[1] = 0x7F, 255            # what row 0 holds must not matter
     table = np.array([[3, 4], [bad, bad], [5, 6]])
-    p = _problem(table, [100, 100, 100], 128, dsa.DSA_BF16, 1)
+    p = _problem(table, [100, 100, 100], topk, dsa.DSA_BF16, 1)
     q = torch.randn(3, 128, 576, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(torch.bfloat16)
-    idx = np.tile(np.where(np.arange(128) < 100, np.arange(128), -1).astype(np.int32), (3, 1))
+    idx = np.tile(np.where(np.arange(topk) < 100, np.arange(topk), -1).astype(np.int32), (3, 1))
     out, lse = torch.zeros(3, 128, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(3, 128, device=DEV)
     ws = torch.zeros(max(256, dsa.dsa_sparse_mla_fp8_workspace_size(p)), dtype=torch.uint8, device=DEV)
     dsa.dsa_sparse_mla_fp8_fwd(p, q, dev(codes), dev(byte), dev(idx), out, lse, ws)
     _expect_bounds()
-    assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))      # (row 0 holds numbers here)
+    assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
     values = ref.cache_values(codes, byte)
     for t, first in ((0, 3 * 64), (2, 5 * 64)):
         o, l, ot, lt = ref.attention(q[t].double().cpu().numpy(), np.arange(first, first + 100), values, byte, 1 / 192 ** 0.5)
         assert np.all(np.abs(out[t].double().cpu().numpy() - o) <= ot) and np.all(np.abs(lse[t].double().cpu().numpy() - l) <= lt)
+
+
+@pytest.mark.parametrize("T", [2, 60])
+def test_attention_of_a_part_whose_pages_are_all_bad(T):
+    """A split of the index row (few tokens) or a whole block of it lists keys on bad pages only."""
+    rng = np.random.default_rng(4)
+    codes, byte = ref.quantise_latent(rng.standard_normal((768, 512)), rng.standard_normal((768, 64)))
+    codes[0] = 0x7F
+    table = np.full((T, 11), 11)
+    table[:] = np.arange(1, 12)
+    table[1, 4:8] = -1                       # keys 256 .. 511 of token 1
+    lens = [704] * T
+    q = torch.randn(T, 128, 576, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV).to(torch.bfloat16)
+    values = ref.cache_values(codes, byte)
+    for topk in (512, 704):                  # the bad block last, and between others
+        p = _problem(table, lens, topk, dsa.DSA_BF16, 1)
+        idx = np.tile(np.arange(topk, dtype=np.int32), (T, 1))
+        out, lse = torch.zeros(T, 128, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(T, 128, device=DEV)
+        ws = torch.zeros(max(256, dsa.dsa_sparse_mla_fp8_workspace_size(p)), dtype=torch.uint8, device=DEV)
+        dsa.dsa_sparse_mla_fp8_fwd(p, q, dev(codes), dev(byte), dev(idx), out, lse, ws)
+        _expect_bounds()
+        for t in (0, 1, T - 1):
+            keys = np.array([k for k in range(topk) if t != 1 or not 256 <= k < 512])
+            o, l, ot, lt = ref.attention(q[t].double().cpu().numpy(), keys + 64, values, byte, 1 / 192 ** 0.5)
+            assert np.all(np.abs(out[t].double().cpu().numpy() - o) <= ot), (topk, t)
+            assert np.all(np.abs(lse[t].double().cpu().numpy() - l) <= lt), (topk, t)
 
 
 @pytest.mark.parametrize("form", [dsa.DSA_BF16, dsa.DSA_E4M3, dsa.DSA_E4M3_UE8M0])
